@@ -176,13 +176,14 @@ def _plain_ce(s):
     z = h @ w.t()
     m = z.amax(1, keepdim=True)
     lse = m + torch.log(torch.exp(z - m).sum(1, keepdim=True))
-    logp = torch.where(valid, (z.gather(1, y) - lse)[:, 0], torch.zeros_like(lse[:, 0]))
+    none = torch.zeros_like(lse[:, 0])
+    out = {"logp": torch.where(valid, (z.gather(1, y) - lse)[:, 0], none), "lse": torch.where(valid, lse[:, 0], none)}
     if not s["backward"]:
-        return {"logp": logp, "lse": lse[:, 0]}
-    a = torch.where(valid, s["weight"], torch.zeros_like(s["weight"]))[:, None]
+        return out
+    a = torch.where(valid, s["weight"], none)[:, None]
     gz = torch.exp(z - lse) * a
     gz.scatter_add_(1, y, -a)
-    return {"logp": logp, "lse": lse[:, 0], "dh": (gz @ w).to(s["h"].dtype), "dw": (gz.t() @ h).to(s["w"].dtype)}
+    return {**out, "dh": (gz @ w).to(s["h"].dtype), "dw": (gz.t() @ h).to(s["w"].dtype)}
 
 
 def _plain_kl(s):
@@ -199,13 +200,14 @@ def _plain_kl(s):
     z = (h @ w.t()) / T
     m = z.amax(1, keepdim=True)
     lse = m + torch.log(torch.exp(z - m).sum(1, keepdim=True))
-    kl = (q * (logq - (z.gather(1, ids) - lse))).sum(1)
+    none = torch.zeros_like(lse[:, 0])
+    out = {"kl": (q * (logq - (z.gather(1, ids) - lse))).sum(1), "lse": torch.where(some[:, 0], lse[:, 0], none)}
     if not s["backward"]:
-        return {"kl": kl, "lse": lse[:, 0]}
-    a = torch.where(some[:, 0], s["weight"], torch.zeros_like(s["weight"]))[:, None] / T
+        return out
+    a = torch.where(some[:, 0], s["weight"], none)[:, None] / T
     gz = torch.exp(z - lse) * a
     gz.scatter_add_(1, ids, -a * q)
-    return {"kl": kl, "lse": lse[:, 0], "dh": (gz @ w).to(s["h"].dtype), "dw": (gz.t() @ h).to(s["w"].dtype)}
+    return {**out, "dh": (gz @ w).to(s["h"].dtype), "dw": (gz.t() @ h).to(s["w"].dtype)}
 
 
 def _plain_embed(s):
@@ -230,12 +232,13 @@ def work(case):
         if case["backward"]:
             b += N * d * o + V * d * gr
         return {"bytes": b, "flops": N * d * (2 if case["backward"] else 1)}
-    b = (N + V) * d * e + 12 * N
-    f = 2 * N * V * d
+    M = max(1, int(N * (1 - case["ignored"])))  # rows with a target: the others need no logits
+    b = (M + V) * d * e + 12 * N
+    f = 2 * M * V * d
     if case["op"] == "kl":
         b += 8 * N * case["K"]
     if case["backward"]:
-        b += (N + V) * d * e + 4 * N
+        b += (N + V) * d * e + 4 * N  # dh and dw whole
         f *= 3
     return {"bytes": b, "flops": f}
 
@@ -280,7 +283,7 @@ def exact(case, seed):
             want.index_put_((n[:, None].expand_as(ids)[ids >= 0], ids[ids >= 0]), q[ids >= 0], accumulate=True)
         lse = torch.logsumexp(z, 1)
         lp = z - lse[:, None]
-        lses.append(lse)
+        lses.append(torch.where(has, lse, torch.zeros_like(lse)))  # a row without a target has none
         if case["op"] == "ce":
             loss.append((want * lp).sum(1))
         else:
