@@ -445,6 +445,94 @@ int32_t rlt_op_prefix_attention_noalloc(const float* q_dev, const void* k_dev, c
 int32_t rlt_op_sample(const float* logits_dev, int32_t B, int32_t V, const rlt_sampling* samp, uint32_t t,
                       int32_t* token_dev, float* logp_dev, float* logmu_dev, void* stream);
 
+/* ------------------------------------------------- vocabulary operators */
+
+/* Operands of the loss over the vocabulary: N rows of h (a readout operand,
+ * report eq. 2.6) against the V rows of w (a readout or embedding matrix),
+ * both row-major in `dtype` with rows ld_* elements apart (ld >= d).  Any N,
+ * V, d and row distance; 0 <= N, 1 <= V, 1 <= d.  Fastest where the bases are
+ * 16-byte aligned and (bf16) ld % 8 == 0; other bf16 operands are repacked.
+ * The logits are
+ *   z[n][v] = sum_k h[n][k] w[v][k],
+ * accumulated in fp32.  They are formed a piece of the vocabulary at a time and never kept. */
+typedef struct rlt_vocab {
+  const void* h;     /* [N][d], device */
+  int64_t ld_h;
+  const void* w;     /* [V][d], device */
+  int64_t ld_w;
+  int32_t N, V, d;
+  int32_t dtype;     /* RLT_DTYPE_BF16 or RLT_DTYPE_F32, of h, w, dh and dw */
+} rlt_vocab;
+
+/* Workspace of the calls below: with ws_dev == NULL nothing is launched and
+ * *ws_bytes receives the bytes the call needs; otherwise *ws_bytes is the size
+ * of ws_dev (256-byte aligned device memory, contents arbitrary).  The memory
+ * belongs to the call until its work on `stream` is done: calls that may
+ * overlap on the GPU, replays of captured graphs among them, need their own.
+ * The calls allocate nothing, wait for nothing on the host, and can be
+ * captured into a graph.  Results do not depend on timing. */
+
+/* Softmax cross entropy over the vocabulary, as rlt_replay_backward's loss:
+ *   lse[n] = log sum_v exp z[n][v],  logp[n] = z[n][target[n]] - lse[n].
+ * A row whose target lies outside [0, V) (-1: a prompt, user or padding row)
+ * has none: logp[n] = lse[n] = 0, and its h is not used.
+ * Errors: RLT_E_INVAL, RLT_E_CAPACITY (workspace too small), RLT_E_CUDA. */
+int32_t rlt_op_cross_entropy(const rlt_vocab* a, const int32_t* target_dev, float* logp_dev, float* lse_dev,
+                             void* ws_dev, size_t* ws_bytes, void* stream);
+
+/* Gradient of L = - sum_n weight[n] logp[n] (weights as rlt_replay_backward:
+ * eqs. 5.1, 5.2 and 5.4 are choices of them), with lse from the forward call on the same
+ * operands:  dz[n][v] = weight[n] (exp(z[n][v] - lse[n]) - [v = target[n]]),
+ * dh = dz w, dw = dz^T h.  dh_dev [N][d] (rows ld_dh apart) is written whole
+ * (zeros for rows without a target or of weight 0, whose h is not used);
+ * dw_dev [V][d] is written whole or, with accumulate_dw, added to.  Either
+ * may be NULL, not both; neither may overlap an operand.  Sums are fp32; with
+ * bf16 operands dz is rounded to bf16 once, as an operand of the two products.
+ * Errors: as rlt_op_cross_entropy. */
+int32_t rlt_op_cross_entropy_backward(const rlt_vocab* a, const int32_t* target_dev, const float* lse_dev,
+                                      const float* weight_dev, void* dh_dev, int64_t ld_dh, void* dw_dev,
+                                      int64_t ld_dw, int32_t accumulate_dw, void* ws_dev, size_t* ws_bytes,
+                                      void* stream);
+
+/* Distillation from a teacher's top logits (such as the candidates of
+ * rlt_sampling): ids_dev [N][K] and teacher_dev [N][K] fp32, 1 <= K <= 256.
+ * Slots whose id lies outside [0, V) are empty.  With T = temperature > 0,
+ *   q[n][k] = softmax over the row's slots of teacher[n][k] / T,
+ *   lse[n]  = log sum_v exp(z[n][v] / T),
+ *   kl[n]   = sum_k q[n][k] (log q[n][k] - z[n][ids[n][k]] / T + lse[n]).
+ * An id that stands in several slots counts once per slot.  A row with no
+ * slot, or whose teacher logits are all -inf, has kl[n] = lse[n] = 0 and its h is not used.
+ * Errors: as rlt_op_cross_entropy. */
+int32_t rlt_op_distill(const rlt_vocab* a, const int32_t* ids_dev, const float* teacher_dev, int32_t K,
+                       float temperature, float* kl_dev, float* lse_dev, void* ws_dev, size_t* ws_bytes,
+                       void* stream);
+
+/* Gradient of L = sum_n weight[n] kl[n]: dz[n][v] = weight[n] / T
+ * (exp(z[n][v] / T - lse[n]) - sum_{k: ids[n][k] = v} q[n][k]); the rest as
+ * rlt_op_cross_entropy_backward. */
+int32_t rlt_op_distill_backward(const rlt_vocab* a, const int32_t* ids_dev, const float* teacher_dev, int32_t K,
+                                float temperature, const float* lse_dev, const float* weight_dev, void* dh_dev,
+                                int64_t ld_dh, void* dw_dev, int64_t ld_dw, int32_t accumulate_dw, void* ws_dev,
+                                size_t* ws_bytes, void* stream);
+
+/* Embedding lookup (the model's first step, with a scale):
+ * out[n][:] = scale * emb[tok[n]][:] for n < N, emb [V][d] in emb_dtype, out
+ * [N][d] in out_dtype, rows ld_* elements apart; the product is fp32 and
+ * rounded once.  An id outside [0, V) gives a zero row.  Errors: RLT_E_INVAL, RLT_E_CUDA. */
+int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int32_t V, int32_t d,
+                     const int32_t* tok_dev, int32_t N, float scale, void* out_dev, int64_t ld_out,
+                     int32_t out_dtype, void* stream);
+
+/* Its gradient: demb[v][:] = scale * sum of dout[n][:] over the n with tok[n]
+ * = v, added to demb with accumulate, else written whole (zero rows for ids
+ * that do not occur).  The ids are sorted and every row is summed in fp32 in an
+ * order that depends on N, d and the ids alone.  dout [N][d] in dout_dtype,
+ * demb [V][d] in demb_dtype.  Ids outside [0, V) contribute nothing and their dout is not read.
+ * Errors: RLT_E_INVAL, RLT_E_CAPACITY (workspace too small), RLT_E_CUDA. */
+int32_t rlt_op_embed_backward(const void* dout_dev, int64_t ld_dout, int32_t dout_dtype, const int32_t* tok_dev,
+                              int32_t N, int32_t V, int32_t d, float scale, void* demb_dev, int64_t ld_demb,
+                              int32_t demb_dtype, int32_t accumulate, void* ws_dev, size_t* ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- misc */
 
 /* Copies the calling thread's last error text (NUL-terminated, truncated to

@@ -47,6 +47,8 @@ EXPORTED = (
     "rlt_op_sample", "rlt_kernel_launches", "rlt_op_prefix_attention", "rlt_op_prefix_attention_noalloc",
     "rlt_state_export", "rlt_state_import", "rlt_replay_ratios", "rlt_replay_backward", "rlt_grad_read",
     "rlt_grad_zero", "rlt_test_bounded_wait", "rlt_state_positions", "rlt_append_spans", "rlt_backward_release",
+    "rlt_op_cross_entropy", "rlt_op_cross_entropy_backward", "rlt_op_distill", "rlt_op_distill_backward",
+    "rlt_op_embed", "rlt_op_embed_backward",
 )
 
 
@@ -82,8 +84,16 @@ class StateInfo(ctypes.Structure):
                 ("has_pending", ctypes.c_int32), ("uniform", ctypes.c_int32)]
 
 
+class Vocab(ctypes.Structure):
+    _fields_ = [("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64), ("w", ctypes.c_void_p), ("ld_w", ctypes.c_int64),
+                ("N", ctypes.c_int32), ("V", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
+_f32 = ctypes.c_float
+_sz = ctypes.POINTER(ctypes.c_size_t)
 _sig = {
     "rlt_init_weights": [ctypes.POINTER(Config), ctypes.c_uint64, ctypes.POINTER(_vp)],
     "rlt_load_weights": [_vp, ctypes.c_char_p, _vp, ctypes.c_size_t],
@@ -113,6 +123,13 @@ _sig = {
     "rlt_op_prefix_attention_noalloc": [_vp, _vp, _vp, ctypes.c_int64, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp,
                                         _vp],
     "rlt_op_sample": [_vp, _i32, _i32, ctypes.POINTER(Sampling), ctypes.c_uint32, _vp, _vp, _vp, _vp],
+    "rlt_op_cross_entropy": [ctypes.POINTER(Vocab), _vp, _vp, _vp, _vp, _sz, _vp],
+    "rlt_op_cross_entropy_backward": [ctypes.POINTER(Vocab), _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _sz, _vp],
+    "rlt_op_distill": [ctypes.POINTER(Vocab), _vp, _vp, _i32, _f32, _vp, _vp, _vp, _sz, _vp],
+    "rlt_op_distill_backward": [ctypes.POINTER(Vocab), _vp, _vp, _i32, _f32, _vp, _vp, _vp, _i64, _vp, _i64, _i32,
+                                _vp, _sz, _vp],
+    "rlt_op_embed": [_vp, _i64, _i32, _i32, _i32, _vp, _i32, _f32, _vp, _i64, _i32, _vp],
+    "rlt_op_embed_backward": [_vp, _i64, _i32, _vp, _i32, _i32, _i32, _f32, _vp, _i64, _i32, _i32, _vp, _sz, _vp],
     "rlt_last_error": [ctypes.c_char_p, ctypes.c_size_t],
     "rlt_check_device": [],
     "rlt_kernel_launches": [ctypes.POINTER(ctypes.c_int64)],
@@ -447,6 +464,159 @@ def rlt_op_sample(logits, sampling: dict, t: int, token, logp=None, logmu=None, 
     _check(_lib.rlt_op_sample(_dev(logits, "torch.float32"), B, V, _sampling(sampling), t,
                               _dev(token, "torch.int32", B), _dev(logp, "torch.float32", B),
                               _dev(logmu, "torch.float32", B), _stream(stream)))
+
+
+# ------------------------------------------------- vocabulary operators
+def _rows2(t, what: str, rows: int | None = None, cols: int | None = None):
+    """(pointer, row distance, dtype) of a CUDA matrix whose rows are
+    contiguous and do not overlap; rows may stand apart (a slice of columns)."""
+    n, d = t.shape if t.dim() == 2 else (-1, -1)
+    if n < 0 or (rows is not None and n != rows) or (cols is not None and d != cols):
+        raise ValueError(f"{what}: expected shape [{'N' if rows is None else rows}, {'d' if cols is None else cols}], "
+                         f"got {tuple(t.shape)}")
+    dt = _DTYPES.get(str(t.dtype))
+    if dt is None:
+        raise ValueError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
+    ld = t.stride(0) if n > 1 else max(d, 1)
+    if not t.is_cuda or (d > 1 and t.stride(1) != 1) or ld < d:
+        raise ValueError(f"{what}: expected a CUDA matrix with contiguous rows")
+    return t.data_ptr(), ld, dt
+
+
+def _vec(t, dtype_name: str, shape: tuple, what: str):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    return _dev(t, dtype_name)
+
+
+_DTYPES = {"torch.bfloat16": DTYPE_BF16, "torch.float32": DTYPE_F32}
+
+
+def _same_device(*tensors):
+    """The operators run on the current device: tensors elsewhere are refused."""
+    import torch
+    at = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != at:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{at}")
+
+
+def _with_workspace(call, like, workspace, stream) -> None:
+    """call(ws, size*, stream) with the caller's workspace (a uint8 CUDA
+    tensor) or one of the size the call asks for, from torch's allocator on
+    the stream the call runs on."""
+    st = _stream(stream)
+    if workspace is None:
+        need = ctypes.c_size_t()
+        _check(call(None, ctypes.byref(need), st))
+        import torch
+        n = max(need.value, 256)
+        if stream is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(st.value or 0)):
+                workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
+    ptr = _dev(workspace, "torch.uint8")
+    _check(call(ptr, ctypes.byref(ctypes.c_size_t(workspace.numel())), st))
+
+
+def _vocab(h, w):
+    hp, ld_h, dt = _rows2(h, "h")
+    wp, ld_w, wt = _rows2(w, "w", cols=h.shape[1])
+    if wt != dt:
+        raise ValueError(f"h is {h.dtype}, w is {w.dtype}")
+    return Vocab(h=hp, ld_h=ld_h, w=wp, ld_w=ld_w, N=h.shape[0], V=w.shape[0], d=h.shape[1], dtype=dt)
+
+
+def _vocab_grads(h, w, dh, dw):
+    N, d = h.shape
+    out = []
+    for g, like, what, rows in ((dh, h, "dh", N), (dw, w, "dw", w.shape[0])):
+        if g is None:
+            out += [None, 0]
+            continue
+        if g.dtype != like.dtype:
+            raise ValueError(f"{what} is {g.dtype}, its operand {like.dtype}")
+        out += _rows2(g, what, rows=rows, cols=d)[:2]
+    return out
+
+
+def rlt_op_cross_entropy(h, w, target, logp, lse, workspace=None, stream=None) -> None:
+    """logp [N] = log softmax(h @ w^T)[target] and lse [N] (fp32) without kept
+    logits: h [N, d], w [V, d] (bf16 or fp32, rows may stand apart), target
+    int32 [N]; rows whose target is outside [0, V) get 0 in both."""
+    a = _vocab(h, w)
+    N = a.N
+    _same_device(h, w, target, logp, lse, workspace)
+    args = (ctypes.byref(a), _vec(target, "torch.int32", (N,), "target"), _vec(logp, "torch.float32", (N,), "logp"),
+            _vec(lse, "torch.float32", (N,), "lse"))
+    _with_workspace(lambda ws, n, st: _lib.rlt_op_cross_entropy(*args, ws, n, st), h, workspace, stream)
+
+
+def rlt_op_cross_entropy_backward(h, w, target, lse, weight, dh=None, dw=None, accumulate: bool = False,
+                                  workspace=None, stream=None) -> None:
+    """Gradient of -sum(weight * logp) to h and w: dh [N, d], dw [V, d] in the
+    operands' type (either may be None); accumulate adds to dw."""
+    a = _vocab(h, w)
+    N = a.N
+    _same_device(h, w, target, lse, weight, dh, dw, workspace)
+    args = (ctypes.byref(a), _vec(target, "torch.int32", (N,), "target"), _vec(lse, "torch.float32", (N,), "lse"),
+            _vec(weight, "torch.float32", (N,), "weight"), *_vocab_grads(h, w, dh, dw), int(accumulate))
+    _with_workspace(lambda ws, n, st: _lib.rlt_op_cross_entropy_backward(*args, ws, n, st), h, workspace, stream)
+
+
+def _teacher(N, ids, teacher):
+    if ids.dim() != 2:
+        raise ValueError(f"ids: expected shape [{N}, K], got {tuple(ids.shape)}")
+    K = ids.shape[1]
+    return _vec(ids, "torch.int32", (N, K), "ids"), _vec(teacher, "torch.float32", (N, K), "teacher"), K
+
+
+def rlt_op_distill(h, w, ids, teacher, temperature: float, kl, lse, workspace=None, stream=None) -> None:
+    """kl [N] = KL(q || softmax(h @ w^T / T)) with q = softmax(teacher / T) over
+    the K ids of each row (ids int32, teacher fp32, [N, K], K <= 256; ids
+    outside [0, V) are empty slots), and lse [N] of the scaled logits."""
+    a = _vocab(h, w)
+    N = a.N
+    _same_device(h, w, ids, teacher, kl, lse, workspace)
+    args = (ctypes.byref(a), *_teacher(N, ids, teacher), temperature, _vec(kl, "torch.float32", (N,), "kl"),
+            _vec(lse, "torch.float32", (N,), "lse"))
+    _with_workspace(lambda ws, n, st: _lib.rlt_op_distill(*args, ws, n, st), h, workspace, stream)
+
+
+def rlt_op_distill_backward(h, w, ids, teacher, temperature: float, lse, weight, dh=None, dw=None,
+                            accumulate: bool = False, workspace=None, stream=None) -> None:
+    """Gradient of sum(weight * kl) to h and w, as rlt_op_cross_entropy_backward."""
+    a = _vocab(h, w)
+    N = a.N
+    _same_device(h, w, ids, teacher, lse, weight, dh, dw, workspace)
+    args = (ctypes.byref(a), *_teacher(N, ids, teacher), temperature, _vec(lse, "torch.float32", (N,), "lse"),
+            _vec(weight, "torch.float32", (N,), "weight"), *_vocab_grads(h, w, dh, dw), int(accumulate))
+    _with_workspace(lambda ws, n, st: _lib.rlt_op_distill_backward(*args, ws, n, st), h, workspace, stream)
+
+
+def rlt_op_embed(emb, tokens, out, scale: float = 1.0, stream=None) -> None:
+    """out [N, d] = scale * emb[tokens]: emb [V, d], tokens int32 [N]; bf16 or
+    fp32 each; a token outside [0, V) gives a zero row."""
+    N = tokens.numel()
+    ep, ld_e, et = _rows2(emb, "emb")
+    op, ld_o, ot = _rows2(out, "out", rows=N, cols=emb.shape[1])
+    _same_device(emb, tokens, out)
+    _check(_lib.rlt_op_embed(ep, ld_e, et, emb.shape[0], emb.shape[1], _vec(tokens, "torch.int32", (N,), "tokens"), N,
+                             scale, op, ld_o, ot, _stream(stream)))
+
+
+def rlt_op_embed_backward(dout, tokens, demb, scale: float = 1.0, accumulate: bool = False, workspace=None,
+                          stream=None) -> None:
+    """demb [V, d] = scale * the sums of dout [N, d] over each token's rows
+    (sorted by token, fp32 sums, a fixed order); accumulate adds to demb."""
+    N = tokens.numel()
+    V, d = demb.shape if demb.dim() == 2 else (0, 0)
+    gp, ld_g, gt = _rows2(dout, "dout", rows=N, cols=d)
+    ep, ld_e, et = _rows2(demb, "demb")
+    _same_device(dout, tokens, demb, workspace)
+    args = (gp, ld_g, gt, _vec(tokens, "torch.int32", (N,), "tokens"), N, V, d, scale, ep, ld_e, et, int(accumulate))
+    _with_workspace(lambda ws, n, st: _lib.rlt_op_embed_backward(*args, ws, n, st), demb, workspace, stream)
 
 
 def rlt_check_device() -> None:

@@ -32,6 +32,7 @@
 
 #include "internal.h"
 #include "rlt.h"
+#include "vocab.h"
 
 using namespace rlt;
 
@@ -1847,3 +1848,127 @@ extern "C" int32_t rlt_op_prefix_attention_noalloc(const float* q_dev, const voi
   if (e != cudaSuccess) return fail(RLT_E_CUDA, std::string("prefix attention: ") + cudaGetErrorString(e));
   return ok();
 }
+
+// ====================================================================== vocabulary operators
+// rlt_op_cross_entropy, rlt_op_distill, rlt_op_embed and their gradients.
+namespace {
+
+bool known_dtype(int32_t t) { return t == RLT_DTYPE_F32 || t == RLT_DTYPE_BF16; }
+
+// The workspace convention: reports the size (returns 1 with ws null), or checks it.
+int32_t check_workspace(void* ws, size_t* ws_bytes, size_t need, bool* report) {
+  *report = ws == nullptr;
+  if (*report) {
+    *ws_bytes = need;
+    return RLT_OK;
+  }
+  if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(RLT_E_INVAL, "workspace is not 256-byte aligned");
+  if (*ws_bytes < need)
+    return fail(RLT_E_CAPACITY,
+                "workspace of " + std::to_string(*ws_bytes) + " bytes where " + std::to_string(need) + " are needed");
+  return RLT_OK;
+}
+
+int32_t vocab_problem(const rlt_vocab* a, const int32_t* ids, const float* teacher, int32_t K, float temperature,
+                      const size_t* ws_bytes, VocabLoss* p) {
+  if (!a || !ws_bytes) return fail(RLT_E_INVAL, "null operands or workspace size");
+  if (a->N < 0 || a->V < 1 || a->d < 1 || a->ld_h < a->d || a->ld_w < a->d)
+    return fail(RLT_E_INVAL, "vocabulary operands need N >= 0, V >= 1, d >= 1 and ld >= d");
+  if (!known_dtype(a->dtype)) return fail(RLT_E_INVAL, "dtype");
+  if (!a->w || (a->N > 0 && (!a->h || !ids))) return fail(RLT_E_INVAL, "null operand");
+  if (K < 1 || K > 256) return fail(RLT_E_INVAL, "1 <= K <= 256");
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
+    return fail(RLT_E_INVAL, "temperature > 0");
+  *p = VocabLoss{a->h, a->ld_h, a->w, a->ld_w, a->N, a->V, a->d, a->dtype, ids, teacher, K, 1.f / temperature};
+  return RLT_OK;
+}
+
+int32_t vocab_forward_call(const VocabLoss& p, float* loss, float* lse, void* ws, size_t* ws_bytes, void* stream) {
+  if (p.N > 0 && (!loss || !lse)) return fail(RLT_E_INVAL, "null output");
+  bool report;
+  RLT_TRY(check_workspace(ws, ws_bytes, vocab_workspace_bytes(p, 0), &report));
+  if (!report) RLT_CUDA(vocab_forward(p, loss, lse, ws, (cudaStream_t)stream));
+  return ok();
+}
+
+int32_t vocab_backward_call(const VocabLoss& p, const float* lse, const float* weight, void* dh, int64_t ld_dh,
+                            void* dw, int64_t ld_dw, int32_t accumulate_dw, void* ws, size_t* ws_bytes,
+                            void* stream) {
+  if (p.N > 0 && (!lse || !weight)) return fail(RLT_E_INVAL, "null lse or weight");
+  if (!dh && !dw) return fail(RLT_E_INVAL, "no gradient requested");
+  if ((dh && ld_dh < p.d) || (dw && ld_dw < p.d)) return fail(RLT_E_INVAL, "gradient rows need ld >= d");
+  bool report;
+  RLT_TRY(check_workspace(ws, ws_bytes, vocab_workspace_bytes(p, 1), &report));
+  if (!report)
+    RLT_CUDA(vocab_backward(p, lse, weight, dh, ld_dh, dw, ld_dw, accumulate_dw != 0, ws, (cudaStream_t)stream));
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t rlt_op_cross_entropy(const rlt_vocab* a, const int32_t* target_dev, float* logp_dev, float* lse_dev,
+                             void* ws_dev, size_t* ws_bytes, void* stream) {
+  VocabLoss p;
+  RLT_TRY(vocab_problem(a, target_dev, nullptr, 1, 1.f, ws_bytes, &p));
+  return vocab_forward_call(p, logp_dev, lse_dev, ws_dev, ws_bytes, stream);
+}
+
+int32_t rlt_op_cross_entropy_backward(const rlt_vocab* a, const int32_t* target_dev, const float* lse_dev,
+                                      const float* weight_dev, void* dh_dev, int64_t ld_dh, void* dw_dev,
+                                      int64_t ld_dw, int32_t accumulate_dw, void* ws_dev, size_t* ws_bytes,
+                                      void* stream) {
+  VocabLoss p;
+  RLT_TRY(vocab_problem(a, target_dev, nullptr, 1, 1.f, ws_bytes, &p));
+  return vocab_backward_call(p, lse_dev, weight_dev, dh_dev, ld_dh, dw_dev, ld_dw, accumulate_dw, ws_dev, ws_bytes,
+                             stream);
+}
+
+int32_t rlt_op_distill(const rlt_vocab* a, const int32_t* ids_dev, const float* teacher_dev, int32_t K,
+                       float temperature, float* kl_dev, float* lse_dev, void* ws_dev, size_t* ws_bytes,
+                       void* stream) {
+  VocabLoss p;
+  RLT_TRY(vocab_problem(a, ids_dev, teacher_dev, K, temperature, ws_bytes, &p));
+  if (p.N > 0 && !teacher_dev) return fail(RLT_E_INVAL, "null teacher logits");
+  return vocab_forward_call(p, kl_dev, lse_dev, ws_dev, ws_bytes, stream);
+}
+
+int32_t rlt_op_distill_backward(const rlt_vocab* a, const int32_t* ids_dev, const float* teacher_dev, int32_t K,
+                                float temperature, const float* lse_dev, const float* weight_dev, void* dh_dev,
+                                int64_t ld_dh, void* dw_dev, int64_t ld_dw, int32_t accumulate_dw, void* ws_dev,
+                                size_t* ws_bytes, void* stream) {
+  VocabLoss p;
+  RLT_TRY(vocab_problem(a, ids_dev, teacher_dev, K, temperature, ws_bytes, &p));
+  if (p.N > 0 && !teacher_dev) return fail(RLT_E_INVAL, "null teacher logits");
+  return vocab_backward_call(p, lse_dev, weight_dev, dh_dev, ld_dh, dw_dev, ld_dw, accumulate_dw, ws_dev, ws_bytes,
+                             stream);
+}
+
+int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int32_t V, int32_t d,
+                     const int32_t* tok_dev, int32_t N, float scale, void* out_dev, int64_t ld_out,
+                     int32_t out_dtype, void* stream) {
+  if (N < 0 || V < 1 || d < 1 || ld_emb < d || ld_out < d || !emb_dev || (N > 0 && (!tok_dev || !out_dev)))
+    return fail(RLT_E_INVAL, "bad embedding arguments");
+  if (!known_dtype(emb_dtype) || !known_dtype(out_dtype)) return fail(RLT_E_INVAL, "dtype");
+  RLT_CUDA(embed_lookup(emb_dev, ld_emb, emb_dtype, V, d, tok_dev, N, scale, out_dev, ld_out, out_dtype,
+                        (cudaStream_t)stream));
+  return ok();
+}
+
+int32_t rlt_op_embed_backward(const void* dout_dev, int64_t ld_dout, int32_t dout_dtype, const int32_t* tok_dev,
+                              int32_t N, int32_t V, int32_t d, float scale, void* demb_dev, int64_t ld_demb,
+                              int32_t demb_dtype, int32_t accumulate, void* ws_dev, size_t* ws_bytes, void* stream) {
+  if (N < 0 || V < 1 || d < 1 || ld_dout < d || ld_demb < d || !demb_dev || !ws_bytes ||
+      (N > 0 && (!tok_dev || !dout_dev)))
+    return fail(RLT_E_INVAL, "bad embedding gradient arguments");
+  if (!known_dtype(dout_dtype) || !known_dtype(demb_dtype)) return fail(RLT_E_INVAL, "dtype");
+  bool report;
+  RLT_TRY(check_workspace(ws_dev, ws_bytes, embed_backward_workspace_bytes(N, V, d), &report));
+  if (!report)
+    RLT_CUDA(embed_backward(dout_dev, ld_dout, dout_dtype, tok_dev, N, V, d, scale, demb_dev, ld_demb, demb_dtype,
+                            accumulate != 0, ws_dev, (cudaStream_t)stream));
+  return ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,153 @@
+"""Refusals of the vocabulary operators, decided on the host before anything
+is launched, and the workspace convention.  No GPU is needed."""
+import ctypes
+import types
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def rlt():
+    import stateful_decoder_b200 as rlt
+    return rlt
+
+
+P = ctypes.c_void_p(4096)  # a pointer that no refused call follows
+
+
+def operands(rlt, **kw):
+    a = dict(h=4096, ld_h=64, w=4096, ld_w=64, N=3, V=100, d=64, dtype=1)
+    a.update(kw)
+    return rlt.Vocab(**a)
+
+
+def sized(n):
+    return ctypes.byref(ctypes.c_size_t(n))
+
+
+BIG = 1 << 40
+
+
+def test_operands_are_checked(rlt):
+    lib = rlt._lib
+    for bad in (dict(N=-1), dict(V=0), dict(d=0), dict(ld_h=63), dict(ld_w=63), dict(dtype=2), dict(h=None), dict(w=None)):
+        a = ctypes.byref(operands(rlt, **bad))
+        assert lib.rlt_op_cross_entropy(a, P, P, P, P, sized(BIG), None) == rlt.RLT_E_INVAL, bad
+        assert lib.rlt_op_distill(a, P, P, 4, 1.0, P, P, P, sized(BIG), None) == rlt.RLT_E_INVAL, bad
+        assert lib.rlt_op_cross_entropy_backward(a, P, P, P, P, 64, P, 64, 0, P, sized(BIG), None) == rlt.RLT_E_INVAL, bad
+        assert lib.rlt_op_distill_backward(a, P, P, 4, 1.0, P, P, P, 64, P, 64, 0, P, sized(BIG), None) == rlt.RLT_E_INVAL, bad
+    a = ctypes.byref(operands(rlt))
+    assert lib.rlt_op_cross_entropy(None, P, P, P, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert lib.rlt_op_cross_entropy(a, None, P, P, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert lib.rlt_op_cross_entropy(a, P, None, P, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert lib.rlt_op_cross_entropy(a, P, P, None, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert lib.rlt_op_cross_entropy(a, P, P, P, P, None, None) == rlt.RLT_E_INVAL
+    for K, T in ((0, 1.0), (257, 1.0), (4, 0.0), (4, -1.0), (4, float("nan")), (4, float("inf")), (4, 1e-45)):
+        assert lib.rlt_op_distill(a, P, P, K, T, P, P, P, sized(BIG), None) == rlt.RLT_E_INVAL, (K, T)
+    assert lib.rlt_op_distill(a, P, None, 4, 1.0, P, P, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    back = lib.rlt_op_cross_entropy_backward
+    assert back(a, P, None, P, P, 64, P, 64, 0, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert back(a, P, P, None, P, 64, P, 64, 0, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert back(a, P, P, P, None, 0, None, 0, 0, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert back(a, P, P, P, P, 63, P, 64, 0, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert back(a, P, P, P, P, 64, P, 63, 0, P, sized(BIG), None) == rlt.RLT_E_INVAL
+
+
+def test_embedding_arguments_are_checked(rlt):
+    lib = rlt._lib
+    good = [P, 64, 1, 100, 64, P, 3, 1.0, P, 64, 0, None]
+    for at, bad in ((0, None), (1, 63), (2, 2), (3, 0), (4, 0), (5, None), (6, -1), (8, None), (9, 63), (10, -1)):
+        args = list(good)
+        args[at] = bad
+        assert lib.rlt_op_embed(*args) == rlt.RLT_E_INVAL, at
+    good = [P, 64, 1, P, 3, 100, 64, 1.0, P, 64, 0, 0, P, sized(BIG), None]
+    for at, bad in ((0, None), (1, 63), (2, 7), (3, None), (4, -1), (5, 0), (6, 0), (8, None), (9, 63), (10, 2), (13, None)):
+        args = list(good)
+        args[at] = bad
+        assert lib.rlt_op_embed_backward(*args) == rlt.RLT_E_INVAL, at
+
+
+def test_workspace_convention(rlt):
+    """A null workspace reports the size; a short or misaligned one is refused."""
+    lib = rlt._lib
+    a = ctypes.byref(operands(rlt, N=300, V=5000))
+    n = ctypes.c_size_t()
+    calls = (
+        lambda ws, s: lib.rlt_op_cross_entropy(a, P, P, P, ws, s, None),
+        lambda ws, s: lib.rlt_op_cross_entropy_backward(a, P, P, P, P, 64, P, 64, 0, ws, s, None),
+        lambda ws, s: lib.rlt_op_distill(a, P, P, 50, 0.8, P, P, ws, s, None),
+        lambda ws, s: lib.rlt_op_distill_backward(a, P, P, 50, 0.8, P, P, P, 64, P, 64, 0, ws, s, None),
+    )
+    for call in calls:
+        assert call(None, ctypes.byref(n)) == rlt.RLT_OK
+        assert 0 < n.value < 1 << 32
+        assert call(P, sized(n.value - 1)) == rlt.RLT_E_CAPACITY
+        assert call(ctypes.c_void_p(4096 + 128), sized(n.value)) == rlt.RLT_E_INVAL
+    code, text = rlt.rlt_last_error()
+    assert code == rlt.RLT_E_INVAL and "256" in text
+
+
+def test_workspace_does_not_hold_the_logits(rlt):
+    """The loss over 65,536 rows and 256,000 ids: its logits would take 67 GB in
+    fp32; forward and backward need a few GB at most."""
+    lib = rlt._lib
+    n = ctypes.c_size_t()
+    a = ctypes.byref(operands(rlt, N=65536, V=256000, d=2048, ld_h=2048, ld_w=2048))
+    assert lib.rlt_op_cross_entropy(a, P, P, P, None, ctypes.byref(n), None) == rlt.RLT_OK
+    assert n.value < 2 << 30
+    assert lib.rlt_op_cross_entropy_backward(a, P, P, P, P, 2048, P, 2048, 0, None, ctypes.byref(n), None) == rlt.RLT_OK
+    assert n.value < 4 << 30
+
+
+class _Fake:
+    """A CPU tensor that passes for a CUDA one: what the binding refuses, it
+    refuses by shape, type and stride, before the library sees a pointer."""
+
+    def __init__(self, t):
+        self.t, self.is_cuda, self.shape, self.dtype = t, True, t.shape, t.dtype
+        self.device = types.SimpleNamespace(index=0)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_binding_refuses_wrong_tensors(rlt, monkeypatch):
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    def f(*shape, dtype=torch.float32):
+        return _Fake(torch.zeros(*shape, dtype=dtype))
+
+    i32, bf = torch.int32, torch.bfloat16
+    h, w, t, o, e = f(4, 8), f(9, 8), f(4, dtype=i32), f(4), f(4)
+    ids, te = f(4, 3, dtype=i32), f(4, 3)
+    calls = [
+        lambda: rlt.rlt_op_cross_entropy(f(4, 7), w, t, o, e),
+        lambda: rlt.rlt_op_cross_entropy(f(4, 8, dtype=bf), w, t, o, e),
+        lambda: rlt.rlt_op_cross_entropy(f(4, 8, dtype=torch.float16), f(9, 8, dtype=torch.float16), t, o, e),
+        lambda: rlt.rlt_op_cross_entropy(_Fake(torch.zeros(8, 4).t()), w, t, o, e),
+        lambda: rlt.rlt_op_cross_entropy(_Fake(torch.zeros(1, 8).expand(4, 8)), w, t, o, e),
+        lambda: rlt.rlt_op_cross_entropy(h, w, f(5, dtype=i32), o, e),
+        lambda: rlt.rlt_op_cross_entropy(h, w, f(4, dtype=torch.int64), o, e),
+        lambda: rlt.rlt_op_cross_entropy(h, w, t, f(3), e),
+        lambda: rlt.rlt_op_cross_entropy(h, w, t, f(4, dtype=bf), e),
+        lambda: rlt.rlt_op_cross_entropy_backward(h, w, t, e, f(3), dh=f(4, 8)),
+        lambda: rlt.rlt_op_cross_entropy_backward(h, w, t, e, o, dh=f(4, 9)),
+        lambda: rlt.rlt_op_cross_entropy_backward(h, w, t, e, o, dh=f(4, 8, dtype=bf)),
+        lambda: rlt.rlt_op_cross_entropy_backward(h, w, t, e, o, dw=f(8, 8)),
+        lambda: rlt.rlt_op_distill(h, w, f(4, 3), te, 1.0, o, e),
+        lambda: rlt.rlt_op_distill(h, w, ids, f(4, 2), 1.0, o, e),
+        lambda: rlt.rlt_op_distill(h, w, f(12, dtype=i32), te, 1.0, o, e),
+        lambda: rlt.rlt_op_embed(w, f(4, dtype=torch.int64), f(4, 8)),
+        lambda: rlt.rlt_op_embed(w, t, f(4, 7)),
+        lambda: rlt.rlt_op_embed_backward(f(5, 8), t, w),
+        lambda: rlt.rlt_op_embed_backward(f(4, 8), t, f(9, 8, dtype=torch.float16)),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    far = f(9, 8)
+    far.device = types.SimpleNamespace(index=1)
+    with pytest.raises(ValueError, match="current device"):
+        rlt.rlt_op_cross_entropy(h, far, t, o, e)
