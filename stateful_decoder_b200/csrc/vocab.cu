@@ -1,26 +1,33 @@
 // vocab.cu -- softmax cross entropy and distillation over a large vocabulary
-// without kept logits (launchers in vocab.h).
+// without kept logits (launchers in vocab.h, contraction in vocab_gemm.cuh).
 //
-// z[n][v] = inv_t * sum_k h[n][k] w[v][k].  Forward: every vocabulary tile
-// leaves (max, sum of exponentials) per row, joined in tile order into
-// lse[n].  Backward, one piece of the vocabulary at a time: g[n][v] = c[n]
-// (exp(z - lse[n]) - q[n][v]) into a buffer of the piece's width, then
-// dh += g w and dw = g^T h.  The piece bounds the buffer; the logits are
-// recomputed, never kept.
+// z[n][v] = inv_t * sum_k h[n][k] w[v][k].  Forward: every tile of the logits
+// leaves (maximum, sum of exponentials) per row and 128 columns, joined in
+// column order into lse[n].  Backward, one piece of the vocabulary at a time:
+// g[n][v] = c[n] (exp(z - lse[n]) - q[n][v]) as bf16 into a buffer of the
+// piece's width, then dh += g w and dw = g^T h.  The piece bounds the buffer;
+// the logits are recomputed, never kept.
+//
+// Rows that take no part (no target, an empty list, weight 0 in the backward)
+// are left out before the contractions: the rows that remain are gathered, in
+// order, into one bf16 operand, and every extent follows their count on the
+// device.
 #include <math.h>
 
 #include <algorithm>
 
 #include "vocab.h"
+#include "vocab_gemm.cuh"
 
 namespace rlt {
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kNoId = 0x7fffffff;
+using namespace vocab_tc;
+
 constexpr int kMaxK = 256;
 
-__host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
 // ------------------------------------------------------------------ teacher lists
 // One warp per row: q = softmax(teacher * inv_t) over the valid slots, the
@@ -86,174 +93,263 @@ __global__ void __launch_bounds__(128) teacher_prep_kernel(const int32_t* ids, c
   if (lane == 0) some[n] = has ? 1.f : 0.f;
 }
 
-// A row's list as the tile kernels see it.
-struct RowList {
-  const int32_t* ids;  // ascending when K > 1
-  const float* q;      // null: 1
-  const float* some;   // null: the row takes part if its one id is in [0, V)
-  int K;
-};
-__device__ __forceinline__ bool takes_part(const RowList& r, int64_t n, int V) {
-  if (r.some) return r.some[n] != 0.f;
-  const int32_t id = r.ids[n];
-  return id >= 0 && id < V;
-}
-
-// ------------------------------------------------------------------ contractions
-// C[m][n] = sum_k A(m, k) B(n, k) in fp32 over 64 x 64 tiles.
-struct Operand {
-  const void* p;
-  int64_t s_row, s_k;  // strides in elements
-  int bf;
-  __device__ __forceinline__ float at(int64_t row, int64_t k) const {
-    const int64_t o = row * s_row + k * s_k;
-    return bf ? __bfloat162float(static_cast<const bf16*>(p)[o]) : static_cast<const float*>(p)[o];
-  }
-};
-
-__device__ __forceinline__ void tile_product(const Operand& A, const Operand& B, int64_t m0, int64_t n0, int64_t M,
-                                             int64_t N, int64_t K, const float* k_mask, float (*acc)[4],
-                                             float (*as)[kTile + 1], float (*bs)[kTile + 1]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int64_t k0 = 0; k0 < K; k0 += 16) {
-    for (int i = threadIdx.x; i < 16 * kTile; i += 256) {
-      const int kk = i & 15, r = i >> 4;
-      const bool on = k0 + kk < K && (k_mask == nullptr || k_mask[k0 + kk] != 0.f);
-      as[kk][r] = on && m0 + r < M ? A.at(m0 + r, k0 + kk) : 0.f;
-      bs[kk][r] = on && n0 + r < N ? B.at(n0 + r, k0 + kk) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[kk][ty * 4 + i], bs[kk][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-}
-
-// Logit tile of rows m0.. and vocabulary n0..: statistics (g null) or the
-// piece's gradient g[n][v - v_base].
-__global__ void __launch_bounds__(256) logits_kernel(Operand h, Operand w, int N, int V, int d, float inv_t,
-                                                     RowList list, int v_base, int v_end, float2* part, float* zsel,
-                                                     const float* lse, const float* c, float* g, int64_t ld_g) {
-  griddep_enter();
-  __shared__ float as[16][kTile + 1], bs[16][kTile + 1];
-  __shared__ float tile[kTile][kTile + 1];
-  const int64_t m0 = (int64_t)blockIdx.y * kTile, n0 = v_base + (int64_t)blockIdx.x * kTile;
-  float acc[4][4] = {};
-  tile_product(h, w, m0, n0, N, V, d, nullptr, acc, as, bs);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) tile[ty * 4 + i][tx * 4 + j] = acc[i][j] * inv_t;
-  __syncthreads();
-  const int64_t n = m0 + threadIdx.x;
-  if (threadIdx.x >= kTile || n >= N) return;
-  float* z = tile[threadIdx.x];
-  const int cols = (int)min((int64_t)kTile, v_end - n0);
-  if (g == nullptr) {
-    float m = -INFINITY, s = 0.f;
-    for (int j = 0; j < cols; ++j) m = fmaxf(m, z[j]);
-    const float mm = m > -INFINITY ? m : 0.f;
-    for (int j = 0; j < cols; ++j) s += expf(z[j] - mm);
-    part[(int64_t)blockIdx.x * N + n] = make_float2(m, s);
-    for (int k = 0; k < list.K; ++k) {
-      const int64_t j = list.ids[n * list.K + k] - n0;
-      if (j >= 0 && j < cols) zsel[n * list.K + k] = z[j];
-    }
-  } else {
-    const float cn = c[n], l = lse[n];
-    if (cn == 0.f) {
-      for (int j = 0; j < cols; ++j) z[j] = 0.f;
-    } else {
-      for (int j = 0; j < cols; ++j) z[j] = cn * expf(z[j] - l);
-      for (int k = 0; k < list.K; ++k) {
-        const int64_t j = list.ids[n * list.K + k] - n0;
-        if (j >= 0 && j < cols) z[j] -= cn * (list.q ? list.q[n * list.K + k] : 1.f);
-      }
-    }
-    for (int j = 0; j < cols; ++j) g[n * ld_g + (n0 - v_base) + j] = z[j];
-  }
-}
-
-// out[m][n] (+)= A B in the output's type, optionally through an fp32
-// accumulator over the pieces (acc_in: add it; acc_out: leave it there).
-__global__ void __launch_bounds__(256) product_kernel(Operand A, Operand B, int64_t M, int64_t N, int64_t K,
-                                                      const float* k_mask, void* out, int64_t ld_out, int out_bf,
-                                                      int accumulate, const float* acc_in, float* acc_out) {
-  griddep_enter();
-  __shared__ float as[16][kTile + 1], bs[16][kTile + 1];
-  const int64_t m0 = (int64_t)blockIdx.y * kTile, n0 = (int64_t)blockIdx.x * kTile;
-  float acc[4][4] = {};
-  tile_product(A, B, m0, n0, M, N, K, k_mask, acc, as, bs);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= M || n >= N) continue;
-      float x = acc[i][j];
-      if (acc_in) x += acc_in[m * N + n];
-      if (acc_out) {
-        acc_out[m * N + n] = x;
-        continue;
-      }
-      const int64_t o = m * ld_out + n;
-      if (out_bf) {
-        bf16* p = static_cast<bf16*>(out) + o;
-        *p = __float2bfloat16_rn(accumulate ? x + __bfloat162float(*p) : x);
-      } else {
-        float* p = static_cast<float*>(out) + o;
-        *p = accumulate ? x + *p : x;
-      }
-    }
-}
-
 // ------------------------------------------------------------------ rows
-// Joins the tiles' statistics in tile order; loss of every row.
-__global__ void __launch_bounds__(128) join_kernel(const float2* part, int tiles, int N, int V, RowList list,
-                                                   const float* slogq, const float* zsel, float* loss, float* lse) {
+// The rows that take part, in order: row_of[i] -> n, pos_of[n] -> i (or -1),
+// and their count.  Forward (weight null) also writes the zeros of the others.
+__global__ void __launch_bounds__(1024) rows_kernel(RowList list, const float* weight, int N, int V, int32_t* row_of,
+                                                    int32_t* pos_of, int32_t* count, float* loss, float* lse) {
   griddep_enter();
-  const int64_t n = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  if (n >= N) return;
-  if (!takes_part(list, n, V)) {
-    loss[n] = 0.f;
-    lse[n] = 0.f;
-    return;
+  __shared__ int warp_sum_s[32];
+  __shared__ int base_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) base_s = 0;
+  __syncthreads();
+  for (int64_t n0 = 0; n0 < N; n0 += 1024) {
+    const int64_t n = n0 + threadIdx.x;
+    const bool on = n < N && takes_part(list, n, V) && (weight == nullptr || weight[n] != 0.f);
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) warp_sum_s[warp] = __popc(b);
+    __syncthreads();
+    const int base = base_s;
+    int mine = lane < 32 ? warp_sum_s[lane] : 0;
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
+    const int total = __reduce_add_sync(0xffffffffu, mine);
+    const int at = base + before + __popc(b & ((1u << lane) - 1));
+    if (n < N) {
+      pos_of[n] = on ? at : -1;
+      if (on) row_of[at] = (int32_t)n;
+      else if (loss) {
+        loss[n] = 0.f;
+        lse[n] = 0.f;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) base_s = base + total;
+    __syncthreads();
   }
-  float m = -INFINITY;
-  for (int t = 0; t < tiles; ++t) m = fmaxf(m, part[(int64_t)t * N + n].x);
-  float s = 0.f;
-  for (int t = 0; t < tiles; ++t) {
-    const float2 p = part[(int64_t)t * N + n];
-    s += p.x > -INFINITY ? p.y * expf(p.x - m) : (isnan(p.y) ? p.y : 0.f);
+  if (threadIdx.x == 0) *count = base_s;
+}
+
+// 8 elements from column c of a row (zeros past d).
+template <typename T>
+__device__ __forceinline__ void row8(const T* row, int c, int d, bool vec, float* v) {
+  if (vec && c + 8 <= d) {
+    load8(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < d ? to_f32(row[c + j]) : 0.f;
   }
-  const float l = m + logf(s);
-  lse[n] = l;
+}
+// The bf16 planes of 8 elements: x0 = bf16(x), x1 = bf16(x - x0), ...; their
+// sum is x to 24 bits.
+__device__ __forceinline__ void planes8(bf16* dst, int64_t plane, int planes, float* v) {
+  for (int p = 0; p < planes; ++p) {
+    store8(dst + p * plane, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] -= to_f32(from_f32<bf16>(v[j]));
+  }
+}
+
+// One warp per row.  out row pos_of[n] (or n) = h row n as bf16 planes; rows
+// that take no part get a zero dh row instead; the 128 warps behind the last
+// row write zero rows up to the next multiple of 128.
+template <typename T>
+__global__ void __launch_bounds__(256) gather_kernel(const T* x, int64_t ld, int64_t rows, int d, int vec,
+                                                     const int32_t* pos_of, const int32_t* count, bf16* out,
+                                                     int64_t ld_out, int64_t plane, int planes, T* zero,
+                                                     int64_t ld_zero) {
+  griddep_enter();
+  const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (n < rows) {
+    const int64_t i = pos_of ? pos_of[n] : n;
+    if (i < 0) {
+      if (zero)
+        for (int c = lane; c < d; c += 32) zero[n * ld_zero + c] = from_f32<T>(0.f);
+      return;
+    }
+    for (int c = lane * 8; c < d; c += 256) {
+      float v[8];
+      row8(x + n * ld, c, d, vec, v);
+      planes8(out + i * ld_out + c, plane, planes, v);
+    }
+  } else if (count && n < rows + 128) {
+    const int64_t i = *count + (n - rows);
+    if (i >= (*count + 127) / 128 * 128) return;
+    for (int c = lane * 8; c < d; c += 256) {
+      float v[8] = {};
+      planes8(out + i * ld_out + c, plane, planes, v);
+    }
+  }
+}
+
+// Joins the statistics of a row's column groups; the row's loss.  A block has
+// 32 rows (x) by 32 groups of column groups (y); the order is fixed.
+__global__ void __launch_bounds__(1024) join_kernel(const float2* part, int parts, int64_t ld, int N,
+                                                    const int32_t* row_of, const int32_t* count, int V, RowList list,
+                                                    const float* slogq, const float* zsel, float* loss, float* lse) {
+  griddep_enter();
+  __shared__ float ms[32][33], ss[32][33];
+  const int x = threadIdx.x, y = threadIdx.y;
+  const int64_t i = (int64_t)blockIdx.x * 32 + x;
+  const int rows = count ? *count : N;
+  const bool in = i < rows;
+  float m = -INFINITY, s = 0.f;
+  if (in) {
+    for (int t = y; t < parts; t += 32) {
+      const float2 p = part[(int64_t)t * ld + i];
+      const float mn = fmaxf(m, p.x);
+      const float a = m > -INFINITY ? expf(m - mn) : (isnan(s) ? s : 0.f);
+      const float b = p.x > -INFINITY ? expf(p.x - mn) : (isnan(p.y) ? p.y : 0.f);
+      s = s * a + p.y * b;
+      m = mn;
+    }
+  }
+  ms[y][x] = m;
+  ss[y][x] = s;
+  __syncthreads();
+  const int64_t n = in && row_of ? row_of[i] : i;
+  const bool on = in && (row_of || takes_part(list, n, V));
+  float M = -INFINITY, total = 0.f;
+  for (int j = 0; j < 32; ++j) M = fmaxf(M, ms[j][x]);
+  for (int j = 0; j < 32; ++j) {
+    const float mj = ms[j][x], sj = ss[j][x];
+    total += mj > -INFINITY ? sj * expf(mj - M) : (isnan(sj) ? sj : 0.f);
+  }
+  const float l = M + logf(total);
   if (list.q == nullptr) {
-    loss[n] = zsel[n] - l;
+    if (y == 0 && in) {
+      lse[n] = on ? l : 0.f;
+      loss[n] = on ? zsel[n] - l : 0.f;
+    }
     return;
   }
   float kl = 0.f;
-  for (int k = 0; k < list.K; ++k) {
-    const int64_t i = n * list.K + k;
-    if (list.ids[i] != kNoId && list.q[i] != 0.f) kl += list.q[i] * (slogq[i] - zsel[i] + l);
+  if (on)
+    for (int k = y; k < list.K; k += 32) {
+      const int64_t e = n * list.K + k;
+      if (list.ids[e] != kNoId && list.q[e] != 0.f) kl += list.q[e] * (slogq[e] - zsel[e] + l);
+    }
+  __syncthreads();
+  ss[y][x] = kl;
+  __syncthreads();
+  if (y == 0 && in) {
+    float r = 0.f;
+    for (int j = 0; j < 32; ++j) r += ss[j][x];
+    lse[n] = on ? l : 0.f;
+    loss[n] = on ? r : 0.f;
   }
-  loss[n] = kl;
 }
 
-// c[n] = weight * inv_t where the row takes part, exactly 0 elsewhere.
-__global__ void coef_kernel(const float* weight, int N, int V, float inv_t, RowList list, float* c) {
+// out rows = the slabs' sum in order (a long K split over the SMs).
+template <typename T>
+__global__ void __launch_bounds__(256) slab_sum_kernel(const float* slab, int splits, int64_t slab_rows, int rows,
+                                                       const int32_t* count, int d, const int32_t* row_of, T* out,
+                                                       int64_t ld, int accumulate) {
   griddep_enter();
-  const int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (n < N) c[n] = takes_part(list, n, V) ? weight[n] * inv_t : 0.f;
+  const int64_t i = blockIdx.y;
+  if (i >= (count ? *count : rows)) return;
+  const int64_t n = row_of ? row_of[i] : i;
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= d) return;
+  float s = 0.f;
+  for (int k = 0; k < splits; ++k) s += slab[((int64_t)k * slab_rows + i) * d + c];
+  T* o = out + n * ld + c;
+  *o = from_f32<T>(accumulate ? s + to_f32(*o) : s);
 }
 
-// ------------------------------------------------------------------ layout
-struct Layout {
-  size_t sid = 0, sq = 0, slogq = 0, some = 0, part = 0, zsel = 0, c = 0, g = 0, dh = 0, total = 0;
-  int tiles = 0, piece = 0, pieces = 0;
+// ------------------------------------------------------------------ host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// A bf16 operand in memory: `planes` matrices [rows][cols], rows ld apart.
+struct Matrix {
+  const bf16* p;
+  int64_t rows, cols, ld, plane;
+  int planes;
 };
+// 64 columns by box_rows rows of one plane, 128-byte swizzle; what lies
+// outside [rows][cols] reads as 0.
+cudaError_t tensor_map(CUtensorMap* tm, const Matrix& m, int box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.planes};
+  cuuint64_t strides[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.planes > 1 ? m.plane : m.rows * m.ld) * 2};
+  cuuint32_t box[3] = {BK, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(m.p), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+#define VOCAB_TRY(...)                \
+  do {                                \
+    cudaError_t e_ = (__VA_ARGS__);   \
+    if (e_ != cudaSuccess) return e_; \
+  } while (0)
+
+template <int KIND, int CG>
+cudaError_t launch(const Matrix& A, const Matrix& B, const Args& a, cudaStream_t st) {
+  using C = Cfg<CG>;
+  constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
+  CUtensorMap ta, tb;
+  VOCAB_TRY(tensor_map(&ta, A, A_MN ? 64 : BM));
+  VOCAB_TRY(tensor_map(&tb, B, B_MN ? 64 : C::B_ROWS));
+  VOCAB_TRY(cudaFuncSetAttribute(vocab_gemm_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+  const int64_t tiles = round_up(a.M, BM * CG) / (BM * CG) * (round_up(a.N, BN) / BN) * a.splits;
+  if (tiles == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, kSmCount / CG) * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_gemm_kernel<KIND, CG>, ta, tb, a);
+  note_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Where things lie in the workspace, and how the work is cut.
+struct Layout {
+  size_t sid = 0, sq = 0, slogq = 0, some = 0, row_of = 0, pos_of = 0, count = 0, h = 0, w = 0, part = 0, zsel = 0,
+         g = 0, dh = 0, dw = 0, total = 0;
+  int planes = 1, terms = 1;
+  bool gather = true, pack_w = false;
+  int64_t rows = 0;  // rows of the gathered operand, a multiple of 256
+  int64_t ld = 0;    // row distance of gathered and packed operands
+  int n_tiles = 0, piece = 0, pieces = 0, dh_splits = 1, dw_splits = 1;
+  bool dh_slab = false;
+};
+
+bool tma_ready(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
+
+// Splits of a long K for a product with too few tiles to fill the SMs, at
+// least eight k-blocks each.
+int split_count(int64_t tiles, int64_t kblocks) {
+  if (tiles * 2 > kSmCount) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kSmCount / tiles, kblocks / 8));
+}
+
 Layout layout(const VocabLoss& p, int backward) {
   Layout L;
   auto take = [&](size_t n) {
@@ -261,27 +357,48 @@ Layout layout(const VocabLoss& p, int backward) {
     L.total += align256(n);
     return at;
   };
-  const size_t rows = (size_t)p.N;
+  const bool f32 = p.dtype == 0;
+  L.planes = f32 ? 3 : 1;
+  L.terms = f32 ? 6 : 1;
+  L.rows = round_up(std::max(p.N, 1), 256);
+  L.ld = round_up(p.d, 8);
+  // A forward pass over one row tile has nothing to gain from leaving rows
+  // out, and its rows do not mix: it reads h where it is.
+  L.gather = f32 || backward || p.N > BM || !tma_ready(p.h, p.ld_h);
+  L.pack_w = f32 || !tma_ready(p.w, p.ld_w);
+  L.n_tiles = (p.V + BN - 1) / BN;
+  const size_t n = (size_t)p.N;
   if (p.teacher) {
-    L.sid = take(rows * p.K * 4);
-    L.sq = take(rows * p.K * 4);
-    L.slogq = take(rows * p.K * 4);
-    L.some = take(rows * 4);
+    L.sid = take(n * p.K * 4);
+    L.sq = take(n * p.K * 4);
+    L.slogq = take(n * p.K * 4);
+    L.some = take(n * 4);
   }
-  L.tiles = (p.V + kTile - 1) / kTile;
+  if (L.gather) {
+    L.row_of = take(n * 4);
+    L.pos_of = take(n * 4);
+    L.count = take(4);
+    L.h = take((size_t)L.planes * L.rows * L.ld * 2);
+  }
+  if (L.pack_w) L.w = take((size_t)L.planes * p.V * L.ld * 2);
   if (!backward) {
-    L.part = take(rows * L.tiles * 8);
-    L.zsel = take(rows * p.K * 4);
+    L.part = take((size_t)2 * L.n_tiles * L.rows * 8);
+    L.zsel = take(n * p.K * 4);
     return L;
   }
-  const size_t budget = (size_t)256 << 20;
-  size_t piece = budget / (std::max<size_t>(rows, 1) * 4) / kTile * kTile;
-  piece = std::max<size_t>(piece, 2048);
-  L.piece = (int)std::min<size_t>(piece, (size_t)L.tiles * kTile);
-  L.pieces = (p.V + L.piece - 1) / L.piece;
-  L.c = take(rows * 4);
-  L.g = take(rows * L.piece * 4);
-  if (L.pieces > 1) L.dh = take(rows * p.d * 4);
+  // The piece: as wide as 256 MB of g allow, at least 2048 columns; equal pieces.
+  const int64_t most = std::max<int64_t>(2048, ((int64_t)256 << 20) / (L.rows * 2 * L.planes) / BN * BN);
+  const int64_t whole = (int64_t)L.n_tiles * BN;
+  L.pieces = (int)((whole + most - 1) / most);
+  L.piece = (int)round_up((whole + L.pieces - 1) / L.pieces, BN);
+  L.pieces = (int)((whole + L.piece - 1) / L.piece);
+  L.g = take((size_t)L.planes * L.rows * L.piece * 2);
+  const int64_t dt = (p.d + BN - 1) / BN;
+  L.dh_splits = split_count(L.rows / BM * dt, (int64_t)L.piece / BK * L.terms);
+  L.dh_slab = L.dh_splits > 1 || L.pieces > 1;
+  if (L.dh_slab) L.dh = take((size_t)L.dh_splits * L.rows * p.d * 4);
+  L.dw_splits = split_count(L.piece / BM * dt, (int64_t)L.rows / BK * L.terms);
+  if (L.dw_splits > 1) L.dw = take((size_t)L.dw_splits * L.piece * p.d * 4);
   return L;
 }
 
@@ -290,22 +407,84 @@ T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
 }
 
-#define VOCAB_TRY(...)                    \
-  do {                                    \
-    cudaError_t e_ = (__VA_ARGS__);       \
-    if (e_ != cudaSuccess) return e_;     \
-  } while (0)
+// What both directions start from: lists, the rows that take part, operands.
+struct Prepared {
+  RowList list;
+  const float* slogq = nullptr;
+  const int32_t *row_of = nullptr, *count = nullptr;
+  Matrix h, w;
+};
 
-// The rows' lists, prepared in the workspace where there is a teacher.
-cudaError_t row_lists(const VocabLoss& p, const Layout& L, void* ws, RowList* r, cudaStream_t st) {
-  *r = RowList{p.ids, nullptr, nullptr, p.K};
-  if (!p.teacher) return cudaSuccess;
-  int32_t* sid = at<int32_t>(ws, L.sid);
-  float *sq = at<float>(ws, L.sq), *slogq = at<float>(ws, L.slogq), *some = at<float>(ws, L.some);
-  VOCAB_TRY(launch_pdl(teacher_prep_kernel, dim3((unsigned)((p.N + 3) / 4)), dim3(128), 0, st, p.ids, p.teacher, p.N,
-                       p.K, p.V, p.inv_t, sid, sq, slogq, some));
-  *r = RowList{sid, sq, some, p.K};
+template <typename T>
+cudaError_t gather_rows(const void* x, int64_t ld, int64_t rows, int d, const int32_t* pos_of, const int32_t* count,
+                        bf16* out, int64_t ld_out, int64_t plane, int planes, void* zero, int64_t ld_zero,
+                        cudaStream_t st) {
+  const int64_t warps = rows + (count ? 128 : 0);
+  const int vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ld % (16 / (int)sizeof(T)) == 0;
+  return launch_pdl(gather_kernel<T>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, static_cast<const T*>(x),
+                    ld, rows, d, vec, pos_of, count, out, ld_out, plane, planes, static_cast<T*>(zero), ld_zero);
+}
+
+cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* weight, float* loss, float* lse,
+                    void* dh, int64_t ld_dh, Prepared* r, cudaStream_t st) {
+  r->list = RowList{p.ids, nullptr, nullptr, p.K};
+  if (p.teacher) {
+    int32_t* sid = at<int32_t>(ws, L.sid);
+    float *sq = at<float>(ws, L.sq), *slogq = at<float>(ws, L.slogq), *some = at<float>(ws, L.some);
+    VOCAB_TRY(launch_pdl(teacher_prep_kernel, dim3((unsigned)((p.N + 3) / 4)), dim3(128), 0, st, p.ids, p.teacher, p.N,
+                         p.K, p.V, p.inv_t, sid, sq, slogq, some));
+    r->list = RowList{sid, sq, some, p.K};
+    r->slogq = slogq;
+  }
+  r->h = Matrix{static_cast<const bf16*>(p.h), p.N, p.d, p.ld_h, 0, 1};
+  r->w = Matrix{static_cast<const bf16*>(p.w), p.V, p.d, p.ld_w, 0, 1};
+  if (L.gather) {
+    int32_t *row_of = at<int32_t>(ws, L.row_of), *pos_of = at<int32_t>(ws, L.pos_of), *count = at<int32_t>(ws, L.count);
+    VOCAB_TRY(launch_pdl(rows_kernel, dim3(1), dim3(1024), 0, st, r->list, weight, p.N, p.V, row_of, pos_of, count,
+                         loss, lse));
+    const int64_t plane = L.rows * L.ld;
+    bf16* h = at<bf16>(ws, L.h);
+    VOCAB_TRY((p.dtype ? gather_rows<bf16> : gather_rows<float>)(p.h, p.ld_h, p.N, p.d, pos_of, count, h, L.ld, plane,
+                                                                 L.planes, dh, ld_dh, st));
+    r->row_of = row_of;
+    r->count = count;
+    r->h = Matrix{h, L.rows, p.d, L.ld, plane, L.planes};
+  }
+  if (L.pack_w) {
+    const int64_t plane = (int64_t)p.V * L.ld;
+    bf16* w = at<bf16>(ws, L.w);
+    VOCAB_TRY((p.dtype ? gather_rows<bf16> : gather_rows<float>)(p.w, p.ld_w, p.V, p.d, nullptr, nullptr, w, L.ld,
+                                                                 plane, L.planes, nullptr, 0, st));
+    r->w = Matrix{w, p.V, p.d, L.ld, plane, L.planes};
+  }
   return cudaSuccess;
+}
+
+Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
+  Args a{};
+  a.terms = L.terms;
+  a.splits = 1;
+  a.list = r.list;
+  a.row_of = r.row_of;
+  a.V = p.V;
+  a.scale = p.inv_t;
+  return a;
+}
+
+template <typename T>
+cudaError_t slab_sum(const float* slab, int splits, int64_t slab_rows, int rows, const int32_t* count, int d,
+                     const int32_t* row_of, void* out, int64_t ld, int accumulate, cudaStream_t st) {
+  // grid.y is bounded by the slab's own rule: few tiles, so few rows
+  return launch_pdl(slab_sum_kernel<T>, dim3((unsigned)((d + 255) / 256), (unsigned)rows), dim3(256), 0, st, slab,
+                    splits, slab_rows, rows, count, d, row_of, static_cast<T*>(out), ld, accumulate);
+}
+
+void typed_output(Args* a, void* out, int64_t ld, int dtype, int accumulate) {
+  a->out = out;
+  a->ld_out = ld;
+  a->out_bf16 = dtype;
+  a->accumulate = accumulate;
+  a->vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ld % (dtype ? 8 : 4) == 0;
 }
 
 }  // namespace
@@ -315,52 +494,86 @@ size_t vocab_workspace_bytes(const VocabLoss& p, int backward) { return layout(p
 cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws, cudaStream_t st) {
   if (p.N == 0) return cudaSuccess;
   const Layout L = layout(p, 0);
-  RowList list;
-  VOCAB_TRY(row_lists(p, L, ws, &list, st));
-  const Operand h{p.h, p.ld_h, 1, p.dtype}, w{p.w, p.ld_w, 1, p.dtype};
-  float2* part = at<float2>(ws, L.part);
-  float* zsel = at<float>(ws, L.zsel);
-  VOCAB_TRY(launch_pdl(logits_kernel, dim3((unsigned)L.tiles, (unsigned)((p.N + kTile - 1) / kTile)), dim3(256), 0, st,
-                       h, w, p.N, p.V, p.d, p.inv_t, list, 0, p.V, part, zsel, (const float*)nullptr,
-                       (const float*)nullptr, (float*)nullptr, (int64_t)0));
-  return launch_pdl(join_kernel, dim3((unsigned)((p.N + 127) / 128)), dim3(128), 0, st, part, L.tiles, p.N, p.V, list,
-                    p.teacher ? at<float>(ws, L.slogq) : nullptr, zsel, loss, lse);
+  Prepared r;
+  VOCAB_TRY(prepare(p, L, ws, nullptr, loss, lse, nullptr, 0, &r, st));
+  Args a = args_of(p, L, r);
+  a.M = p.N;
+  a.m_count = r.count;
+  a.N = p.V;
+  a.K = p.d;
+  a.part = at<float2>(ws, L.part);
+  a.part_ld = L.rows;
+  a.zsel = at<float>(ws, L.zsel);
+  VOCAB_TRY((launch<STATS, 1>(r.h, r.w, a, st)));
+  return launch_pdl(join_kernel, dim3((unsigned)((p.N + 31) / 32)), dim3(32, 32), 0, st, (const float2*)a.part,
+                    2 * L.n_tiles, L.rows, p.N, r.row_of, r.count, p.V, r.list, r.slogq, (const float*)a.zsel, loss,
+                    lse);
 }
 
 cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* weight, void* dh, int64_t ld_dh,
                            void* dw, int64_t ld_dw, int accumulate_dw, void* ws, cudaStream_t st) {
+  const size_t e = p.dtype ? 2 : 4;
   if (p.N == 0) {
     if (!dw || accumulate_dw) return cudaSuccess;
-    const size_t e = p.dtype ? 2 : 4;
     return cudaMemset2DAsync(dw, ld_dw * e, 0, p.d * e, p.V, st);
   }
   const Layout L = layout(p, 1);
-  RowList list;
-  VOCAB_TRY(row_lists(p, L, ws, &list, st));
-  float *c = at<float>(ws, L.c), *g = at<float>(ws, L.g);
-  float* acc = L.pieces > 1 ? at<float>(ws, L.dh) : nullptr;
-  VOCAB_TRY(launch_pdl(coef_kernel, dim3((unsigned)((p.N + 255) / 256)), dim3(256), 0, st, weight, p.N, p.V, p.inv_t,
-                       list, c));
-  const size_t e = p.dtype ? 2 : 4;
-  const unsigned rt = (unsigned)((p.N + kTile - 1) / kTile), dt = (unsigned)((p.d + kTile - 1) / kTile);
+  Prepared r;
+  VOCAB_TRY(prepare(p, L, ws, weight, nullptr, nullptr, dh, ld_dh, &r, st));
+  bf16* g = at<bf16>(ws, L.g);
+  float* slab = L.dh_slab ? at<float>(ws, L.dh) : nullptr;
+  const int64_t g_plane = L.rows * L.piece;
   for (int i = 0; i < L.pieces; ++i) {
-    const int v0 = i * L.piece, v1 = std::min(p.V, v0 + L.piece);
-    const int64_t width = v1 - v0;
-    const unsigned vt = (unsigned)((width + kTile - 1) / kTile);
-    const void* w0 = static_cast<const uint8_t*>(p.w) + (int64_t)v0 * p.ld_w * e;
-    VOCAB_TRY(launch_pdl(logits_kernel, dim3(vt, rt), dim3(256), 0, st, Operand{p.h, p.ld_h, 1, p.dtype},
-                         Operand{p.w, p.ld_w, 1, p.dtype}, p.N, p.V, p.d, p.inv_t, list, v0, v1, (float2*)nullptr,
-                         (float*)nullptr, lse, (const float*)c, g, (int64_t)L.piece));
-    if (dh)
-      VOCAB_TRY(launch_pdl(product_kernel, dim3(dt, rt), dim3(256), 0, st, Operand{g, L.piece, 1, 0},
-                           Operand{w0, 1, p.ld_w, p.dtype}, (int64_t)p.N, (int64_t)p.d, width, (const float*)nullptr,
-                           dh, ld_dh, p.dtype, 0, i > 0 ? (const float*)acc : (const float*)nullptr,
-                           i + 1 < L.pieces ? acc : (float*)nullptr));
-    if (dw)
-      VOCAB_TRY(launch_pdl(product_kernel, dim3(dt, vt), dim3(256), 0, st, Operand{g, 1, L.piece, 0},
-                           Operand{p.h, 1, p.ld_h, p.dtype}, width, (int64_t)p.d, (int64_t)p.N, (const float*)c,
-                           (void*)(static_cast<uint8_t*>(dw) + (int64_t)v0 * ld_dw * e), ld_dw, p.dtype,
-                           accumulate_dw, (const float*)nullptr, (float*)nullptr));
+    const int v0 = i * L.piece, width = std::min(p.V - v0, L.piece);
+    const Matrix G{g, L.rows, L.piece, L.piece, g_plane, L.planes};
+    Args a = args_of(p, L, r);
+    a.M = p.N;
+    a.m_count = r.count;
+    a.N = width;
+    a.K = p.d;
+    a.b_row = v0;
+    a.lse = lse;
+    a.weight = weight;
+    a.g = g;
+    a.ld_g = L.piece;
+    a.g_plane = g_plane;
+    a.planes = L.planes;
+    VOCAB_TRY((launch<GRAD, 1>(r.h, r.w, a, st)));
+    if (dh) {
+      const bool last = i + 1 == L.pieces;
+      Args b = args_of(p, L, r);
+      b.M = p.N;
+      b.m_count = r.count;
+      b.N = p.d;
+      b.K = width;
+      b.b_k = v0;
+      b.splits = L.dh_splits;
+      b.acc_in = i > 0 ? slab : nullptr;
+      b.slab_rows = L.rows;
+      if (L.dh_splits > 1 || !last) b.slab = slab;
+      else typed_output(&b, dh, ld_dh, p.dtype, 0);
+      VOCAB_TRY((launch<DH, 1>(G, r.w, b, st)));
+      if (last && L.dh_splits > 1)
+        VOCAB_TRY((p.dtype ? slab_sum<bf16> : slab_sum<float>)(slab, L.dh_splits, L.rows, p.N, r.count, p.d, r.row_of,
+                                                               dh, ld_dh, 0, st));
+    }
+    if (dw) {
+      void* out = static_cast<uint8_t*>(dw) + (int64_t)v0 * ld_dw * e;
+      Args b = args_of(p, L, r);
+      b.row_of = nullptr;
+      b.M = width;
+      b.N = p.d;
+      b.K = p.N;
+      b.k_count = r.count;
+      b.splits = L.dw_splits;
+      b.slab_rows = L.piece;
+      if (L.dw_splits > 1) b.slab = at<float>(ws, L.dw);
+      else typed_output(&b, out, ld_dw, p.dtype, accumulate_dw);
+      VOCAB_TRY((launch<DW, 1>(G, r.h, b, st)));
+      if (L.dw_splits > 1)
+        VOCAB_TRY((p.dtype ? slab_sum<bf16> : slab_sum<float>)(b.slab, L.dw_splits, L.piece, width, nullptr, p.d,
+                                                               nullptr, out, ld_dw, accumulate_dw, st));
+    }
   }
   return cudaSuccess;
 }
