@@ -280,17 +280,18 @@ struct Matrix {
   int64_t rows, cols, ld, plane;
   int planes;
 };
-// 64 columns by box_rows rows of one plane, 128-byte swizzle; what lies
-// outside [rows][cols] reads as 0.
-cudaError_t tensor_map(CUtensorMap* tm, const Matrix& m, int box_rows) {
+// Boxes of box_cols (64: 128-byte swizzle, 32: 64-byte) by box_rows of one
+// plane; what lies outside [rows][cols] reads as 0.
+cudaError_t tensor_map(CUtensorMap* tm, const Matrix& m, int box_rows, int box_cols = BK) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.planes};
   cuuint64_t strides[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.planes > 1 ? m.plane : m.rows * m.ld) * 2};
-  cuuint32_t box[3] = {BK, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
   const CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(m.p), dims, strides, box, step,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box_cols == BK ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -301,14 +302,16 @@ cudaError_t tensor_map(CUtensorMap* tm, const Matrix& m, int box_rows) {
   } while (0)
 
 template <int KIND, int CG>
-cudaError_t launch(const Matrix& A, const Matrix& B, const Args& a, cudaStream_t st) {
+cudaError_t launch(const Matrix& A, const Matrix& B, const Matrix* G, const Args& a, cudaStream_t st) {
   using C = Cfg<CG>;
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
-  CUtensorMap ta, tb;
+  CUtensorMap ta, tb, tg;
   VOCAB_TRY(tensor_map(&ta, A, A_MN ? 64 : BM));
-  VOCAB_TRY(tensor_map(&tb, B, B_MN ? 64 : C::B_ROWS));
+  VOCAB_TRY(tensor_map(&tb, B, B_MN ? 64 : a.bn / CG));
+  if (G) VOCAB_TRY(tensor_map(&tg, *G, 32, 32));
+  else tg = ta;
   VOCAB_TRY(cudaFuncSetAttribute(vocab_gemm_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-  const int64_t tiles = round_up(a.M, BM * CG) / (BM * CG) * (round_up(a.N, BN) / BN) * a.splits;
+  const int64_t tiles = round_up(a.M, BM * CG) / (BM * CG) * (round_up(a.N, a.bn) / a.bn) * a.splits;
   if (tiles == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, kSmCount / CG) * CG));
@@ -324,9 +327,16 @@ cudaError_t launch(const Matrix& A, const Matrix& B, const Args& a, cudaStream_t
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_gemm_kernel<KIND, CG>, ta, tb, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_gemm_kernel<KIND, CG>, ta, tb, tg, a);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Two CTAs per tile (256 rows; each loads half of the columns' operand)
+// wherever there is more than one row tile.
+template <int KIND>
+cudaError_t contract(const Matrix& A, const Matrix& B, const Matrix* G, const Args& a, cudaStream_t st) {
+  return a.M > BM ? launch<KIND, 2>(A, B, G, a, st) : launch<KIND, 1>(A, B, G, a, st);
 }
 
 // Where things lie in the workspace, and how the work is cut.
@@ -337,7 +347,7 @@ struct Layout {
   bool gather = true, pack_w = false;
   int64_t rows = 0;  // rows of the gathered operand, a multiple of 256
   int64_t ld = 0;    // row distance of gathered and packed operands
-  int n_tiles = 0, piece = 0, pieces = 0, dh_splits = 1, dw_splits = 1;
+  int bn = BN, n_tiles = 0, piece = 0, pieces = 0, dh_splits = 1, dw_splits = 1;
   bool dh_slab = false;
 };
 
@@ -367,6 +377,13 @@ Layout layout(const VocabLoss& p, int backward) {
   L.gather = f32 || backward || p.N > BM || !tma_ready(p.h, p.ld_h);
   L.pack_w = f32 || !tma_ready(p.w, p.ld_w);
   L.n_tiles = (p.V + BN - 1) / BN;
+  if (!backward && p.N <= BM) {
+    // One row tile: the work is reading w once.  Columns per tile so that the
+    // tiles fill whole rounds of the SMs evenly.
+    const int rounds = (L.n_tiles + kSmCount - 1) / kSmCount;
+    L.bn = std::max(32, (int)round_up((p.V + kSmCount * rounds - 1) / (kSmCount * rounds), 16));
+    L.n_tiles = (p.V + L.bn - 1) / L.bn;
+  }
   const size_t n = (size_t)p.N;
   if (p.teacher) {
     L.sid = take(n * p.K * 4);
@@ -386,8 +403,8 @@ Layout layout(const VocabLoss& p, int backward) {
     L.zsel = take(n * p.K * 4);
     return L;
   }
-  // The piece: as wide as 256 MB of g allow, at least 2048 columns; equal pieces.
-  const int64_t most = std::max<int64_t>(2048, ((int64_t)256 << 20) / (L.rows * 2 * L.planes) / BN * BN);
+  // The piece: as wide as 512 MB of g allow, at least 2048 columns; equal pieces.
+  const int64_t most = std::max<int64_t>(2048, ((int64_t)512 << 20) / (L.rows * 2 * L.planes) / BN * BN);
   const int64_t whole = (int64_t)L.n_tiles * BN;
   L.pieces = (int)((whole + most - 1) / most);
   L.piece = (int)round_up((whole + L.pieces - 1) / L.pieces, BN);
@@ -463,6 +480,8 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
 Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
   Args a{};
   a.terms = L.terms;
+  a.chunk = p.dtype ? 16 : 4;
+  a.bn = BN;
   a.splits = 1;
   a.list = r.list;
   a.row_of = r.row_of;
@@ -504,7 +523,8 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
   a.part = at<float2>(ws, L.part);
   a.part_ld = L.rows;
   a.zsel = at<float>(ws, L.zsel);
-  VOCAB_TRY((launch<STATS, 1>(r.h, r.w, a, st)));
+  a.bn = L.bn;
+  VOCAB_TRY(contract<STATS>(r.h, r.w, nullptr, a, st));
   return launch_pdl(join_kernel, dim3((unsigned)((p.N + 31) / 32)), dim3(32, 32), 0, st, (const float2*)a.part,
                     2 * L.n_tiles, L.rows, p.N, r.row_of, r.count, p.V, r.list, r.slogq, (const float*)a.zsel, loss,
                     lse);
@@ -534,14 +554,13 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.b_row = v0;
     a.lse = lse;
     a.weight = weight;
-    a.g = g;
-    a.ld_g = L.piece;
-    a.g_plane = g_plane;
-    a.planes = L.planes;
-    VOCAB_TRY((launch<GRAD, 1>(r.h, r.w, a, st)));
+    VOCAB_TRY(L.planes == 1 ? contract<GRAD>(r.h, r.w, &G, a, st) : contract<GRAD3>(r.h, r.w, &G, a, st));
     if (dh) {
       const bool last = i + 1 == L.pieces;
       Args b = args_of(p, L, r);
+      // bf16 gradients: the sum's drift over 4096 of k (8e-6) is far below
+      // their own rounding
+      if (p.dtype) b.chunk = 64;
       b.M = p.N;
       b.m_count = r.count;
       b.N = p.d;
@@ -552,7 +571,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
       b.slab_rows = L.rows;
       if (L.dh_splits > 1 || !last) b.slab = slab;
       else typed_output(&b, dh, ld_dh, p.dtype, 0);
-      VOCAB_TRY((launch<DH, 1>(G, r.w, b, st)));
+      VOCAB_TRY(contract<DH>(G, r.w, nullptr, b, st));
       if (last && L.dh_splits > 1)
         VOCAB_TRY((p.dtype ? slab_sum<bf16> : slab_sum<float>)(slab, L.dh_splits, L.rows, p.N, r.count, p.d, r.row_of,
                                                                dh, ld_dh, 0, st));
@@ -561,6 +580,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
       void* out = static_cast<uint8_t*>(dw) + (int64_t)v0 * ld_dw * e;
       Args b = args_of(p, L, r);
       b.row_of = nullptr;
+      if (p.dtype) b.chunk = 64;
       b.M = width;
       b.N = p.d;
       b.K = p.N;
@@ -569,7 +589,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
       b.slab_rows = L.piece;
       if (L.dw_splits > 1) b.slab = at<float>(ws, L.dw);
       else typed_output(&b, out, ld_dw, p.dtype, accumulate_dw);
-      VOCAB_TRY((launch<DW, 1>(G, r.h, b, st)));
+      VOCAB_TRY(contract<DW>(G, r.h, nullptr, b, st));
       if (L.dw_splits > 1)
         VOCAB_TRY((p.dtype ? slab_sum<bf16> : slab_sum<float>)(b.slab, L.dw_splits, L.piece, width, nullptr, p.d,
                                                                nullptr, out, ld_dw, accumulate_dw, st));

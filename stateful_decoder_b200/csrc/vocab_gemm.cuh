@@ -7,8 +7,8 @@
 // Kinds:
 //   STATS  D = h w^T: per row and 128 columns, the maximum and the sum of
 //          exponentials of z = D * inv_t, and z at the row's listed ids
-//   GRAD   D = h w^T: g = c (exp(z - lse) - q), rounded to bf16 (one plane),
-//          or to three bf16 planes whose sum is g to 2^-24 (fp32 operands)
+//   GRAD   D = h w^T: g = c (exp(z - lse) - q), rounded to bf16
+//   GRAD3  the same as three bf16 planes whose sum is g to 2^-24
 //   DH     D = g w     (A K-major, B MN-major): fp32 partials or typed rows
 //   DW     D = g^T h   (A and B MN-major): fp32 partials or typed rows
 //
@@ -17,7 +17,14 @@
 //
 // A CTA has twelve warps: one issues TMA, one MMA, one owns tensor memory,
 // eight drain a 128 x 256 accumulator (warps 4-7 its first 128 columns, 8-11
-// the others) while the next tile's MMAs fill the second of two.
+// the others) while the MMAs fill the second of two.
+//
+// The tensor cores add to an accumulator towards zero, an error of half a
+// unit in the last place per 16 of k on average, all one way: over k = 2048
+// logits came out 1e-6 short of themselves, over k = 32000 gradients 2e-5.
+// So a sum stays in tensor memory for `chunk` k-blocks only; the epilogue
+// warps add the chunks in registers, rounding to nearest, under the next
+// chunk's MMAs.
 #pragma once
 #include <cuda.h>
 
@@ -30,7 +37,7 @@ constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int kThreads = 384;
 constexpr int kNoId = 0x7fffffff;
 
-enum Kind { STATS, GRAD, DH, DW };
+enum Kind { STATS, GRAD, GRAD3, DH, DW };
 
 // A row's list of (id, probability) as the kernels see it.
 struct RowList {
@@ -50,6 +57,8 @@ struct Args {
   const int32_t* m_count;
   const int32_t* k_count;
   int terms;              // 1 or 6 plane products
+  int chunk;              // k-blocks per tensor-memory sum (of the leading term)
+  int bn;                 // columns per tile, a multiple of 16 up to BN
   int splits;             // K ranges, one fp32 slab each (DH, DW)
   int a_row, a_k, b_row, b_k;  // coordinate offsets of the operands
   // STATS, GRAD
@@ -62,9 +71,6 @@ struct Args {
   float* zsel;            // [rows][K]
   const float* lse;
   const float* weight;
-  bf16* g;                // [planes][.][ld_g]
-  int64_t ld_g, g_plane;
-  int planes;
   // DH, DW
   float* slab;            // fp32 [splits][slab_rows][N]; null: typed output
   int64_t slab_rows;
@@ -81,7 +87,8 @@ struct Cfg {
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = CG == 1 ? 4 : 6;
-  static constexpr int BAR_OFF = STAGES * STAGE;
+  static constexpr int OUT_OFF = STAGES * STAGE;    // 8 warps x two 32 x 32 bf16 boxes
+  static constexpr int BAR_OFF = OUT_OFF + 8 * 4096;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
 };
 
@@ -164,20 +171,18 @@ __device__ __forceinline__ uint32_t cta_rank() {
   return r;
 }
 
-__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
-  uint32_t r[32];
+// 16 accumulator columns of this warp's 32 lanes.
+__device__ __forceinline__ void ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -220,17 +225,33 @@ struct Tile {
   int m, n, kb0, kb1, split;
 };
 
+// Stores a 32 x 32 bf16 box (64-byte swizzle) from shared memory; what lies
+// outside the map is not written.
+__device__ __forceinline__ void store_box(const CUtensorMap* tm, uint32_t src, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tm)),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 template <int CG>
 struct Plan {
   int m_tiles, n_tiles, kb, total_kb, per_split, tiles;
   __device__ __forceinline__ void init(const Args& a) {
     const int M = a.m_count ? *a.m_count : a.M, K = a.k_count ? *a.k_count : a.K;
     m_tiles = (M + BM * CG - 1) / (BM * CG);
-    n_tiles = (a.N + BN - 1) / BN;
+    n_tiles = (a.N + a.bn - 1) / a.bn;
     kb = (K + BK - 1) / BK;
     total_kb = kb * a.terms;
     per_split = (total_kb + a.splits - 1) / a.splits;
     tiles = m_tiles * n_tiles * a.splits;
+  }
+  // End of the tensor-memory sum that starts at c0.  Of six plane products the
+  // first five add up to 2^-8 of the last, and their error counts as little.
+  __device__ __forceinline__ int chunk_end(const Args& a, int c0, int kb1) const {
+    if (a.terms > 1 && c0 < 5 * kb) return min(kb1, min(c0 + 64, 5 * kb));
+    return min(kb1, c0 + a.chunk);
   }
   // Panels of 16 row tiles, columns of tiles inside: the tiles that run
   // together share their operands in L2.
@@ -252,86 +273,94 @@ struct Plan {
 };
 
 // ---------------------------------------------------------------- epilogues
-// Each handles 128 columns from `col` (within the tile's N extent) of one row
-// per thread; acc(c, v) reads 32 accumulator columns.
-template <typename Acc>
+// Each handles the 128 columns from n_tile * BN + half * 128 of one row per
+// thread, in registers.
 __device__ __forceinline__ void stats_epilogue(const Args& a, int64_t i, int64_t n, bool on, int n_tile, int half,
-                                               int v0, int pos, Acc acc) {
+                                               int v0, int pos, float (&x)[4][32]) {
   const float s2 = a.scale * kLog2e;
-  float m = -INFINITY, s = 0.f;
-  const int cols = min(128, a.N - (n_tile * BN + half * 128));
+  const int cols = min(min(128, a.bn - half * 128), a.N - (n_tile * a.bn + half * 128));
   int next = on && pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
-#pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
-    if (c >= cols) break;
-    float v[32];
-    acc(c, v);
-    while (next >= v0 + c && next < v0 + c + 32) {
-      a.zsel[n * a.list.K + pos] = pick(v, next - v0 - c) * a.scale;
+  float m = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    while (next >= v0 + c * 32 && next < v0 + min(c * 32 + 32, cols)) {
+      a.zsel[n * a.list.K + pos] = pick(x[c], next - v0 - c * 32) * a.scale;
       next = ++pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
     }
-    float cm = -INFINITY;
-    if (c + 32 <= cols) {
+    if (c * 32 + 32 > cols) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) cm = fmaxf(cm, v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (c + j >= cols) v[j] = -INFINITY;
-        cm = fmaxf(cm, v[j]);
-      }
+      for (int j = 0; j < 32; ++j)
+        if (c * 32 + j >= cols) x[c][j] = -INFINITY;
     }
-    const float mn = fmaxf(m, cm);
-    const float sub = mn > -INFINITY ? mn * s2 : 0.f;
-    float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) t[j & 3] += ex2(fmaf(v[j], s2, -sub));
-    s = s * (m > -INFINITY ? ex2(fmaf(m, s2, -sub)) : (isnan(s) ? s : 0.f)) + ((t[0] + t[1]) + (t[2] + t[3]));
-    m = mn;
+    for (int j = 0; j < 32; ++j) m = fmaxf(m, x[c][j]);
   }
-  if (on) a.part[(int64_t)(n_tile * 2 + half) * a.part_ld + i] = make_float2(m * a.scale, s);
+  const float sub = m > -INFINITY ? m * s2 : 0.f;
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 32; ++j) t[j & 3] += ex2(fmaf(x[c][j], s2, -sub));
+  if (on)
+    a.part[(int64_t)(n_tile * 2 + half) * a.part_ld + i] =
+        make_float2(m * a.scale, cols > 0 ? (t[0] + t[1]) + (t[2] + t[3]) : 0.f);
 }
 
-template <typename Acc>
-__device__ __forceinline__ void grad_epilogue(const Args& a, int64_t i, int64_t n, bool on, int n_tile, int half,
-                                              int v0, int pos, Acc acc) {
+// Every warp writes its 32 rows as 32 x 32 boxes through shared memory: stores
+// from the registers would touch 32 lines each.
+template <int PLANES>
+__device__ __forceinline__ void grad_epilogue(const Args& a, const CUtensorMap* tm, uint32_t stage, int64_t i0,
+                                              int lane, int64_t n, bool on, int n_tile, int half, int v0, int pos,
+                                              float (&x)[4][32]) {
   const float s2 = a.scale * kLog2e;
-  const int cols = min(128, a.N - (n_tile * BN + half * 128));
+  const int col0 = n_tile * BN + half * 128;
+  const int cols = min(128, a.N - col0);
   const float cw = on ? a.weight[n] * a.scale : 0.f;
   const float sub = on ? a.lse[n] * kLog2e : 0.f;
   int next = on && pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
-  bf16* grow = a.g + i * a.ld_g + n_tile * BN + half * 128;
-#pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
-    float v[32];
-    acc(c, v);
+  const uint32_t row = (uint32_t)lane * 64, sw = (uint32_t)(lane >> 1) & 3u;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float* v = x[c];
     if (on) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = cw * ex2(fmaf(v[j], s2, -sub));
-      while (next >= v0 + c && next < v0 + c + 32) {
-        sub_at(v, next - v0 - c, cw * (a.list.q ? a.list.q[n * a.list.K + pos] : 1.f));
+      while (next >= v0 + c * 32 && next < v0 + c * 32 + 32) {
+        sub_at(v, next - v0 - c * 32, cw * (a.list.q ? a.list.q[n * a.list.K + pos] : 1.f));
         next = ++pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
       }
-      if (c + 32 > cols) {
+      if (c * 32 + 32 > cols) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : 0.f;
+        for (int j = 0; j < 32; ++j) v[j] = c * 32 + j < cols ? v[j] : 0.f;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = 0.f;
     }
-#pragma unroll 1
-    for (int p = 0; p < a.planes; ++p) {
-      uint4* dst = reinterpret_cast<uint4*>(grow + p * a.g_plane + c);
-      uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        w[j] = pack2(v[2 * j], v[2 * j + 1]);
-        v[2 * j] -= __uint_as_float(w[j] << 16);
-        v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int p = 0; p < PLANES; ++p) {
+      const uint32_t buf = stage + (uint32_t)((c * PLANES + p) & 1) * 2048;
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float* u = v + j * 8 + 2 * e;
+          w[e] = pack2(u[0], u[1]);
+          if (p + 1 < PLANES) {
+            u[0] -= __uint_as_float(w[e] << 16);
+            u[1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+          }
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + row + (((uint32_t)j ^ sw) << 4)), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) store_box(tm, buf, col0 + c * 32, (int)i0, p);
     }
   }
 }
@@ -356,30 +385,27 @@ __device__ __forceinline__ void store_row32(OT* o, float* v, int left, bool vec,
   }
 }
 
-template <typename Acc>
 __device__ __forceinline__ void product_epilogue(const Args& a, int64_t i, int64_t n, bool on, int n_tile, int half,
-                                                 int split, Acc acc) {
+                                                 int split, float (&x)[4][32]) {
+  if (!on) return;
   const int col0 = n_tile * BN + half * 128;
   const int64_t slab = ((int64_t)split * a.slab_rows + i) * a.N + col0;
-#pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
-    const int left = a.N - col0 - c;
-    if (left <= 0) break;
-    float v[32];
-    acc(c, v);
-    if (!on) continue;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int left = a.N - col0 - c * 32;
+    float* v = x[c];
     if (a.acc_in) {
-      const float* p = a.acc_in + slab + c;
+      const float* p = a.acc_in + slab + c * 32;
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (j < left) v[j] += p[j];
     }
     if (a.slab) {
-      store_row32(a.slab + slab + c, v, left, (a.N & 3) == 0, false);
+      store_row32(a.slab + slab + c * 32, v, left, (a.N & 3) == 0, false);
     } else if (a.out_bf16) {
-      store_row32(static_cast<bf16*>(a.out) + n * a.ld_out + col0 + c, v, left, a.vec, a.accumulate);
+      store_row32(static_cast<bf16*>(a.out) + n * a.ld_out + col0 + c * 32, v, left, a.vec, a.accumulate);
     } else {
-      store_row32(static_cast<float*>(a.out) + n * a.ld_out + col0 + c, v, left, a.vec, a.accumulate);
+      store_row32(static_cast<float*>(a.out) + n * a.ld_out + col0 + c * 32, v, left, a.vec, a.accumulate);
     }
   }
 }
@@ -387,7 +413,8 @@ __device__ __forceinline__ void product_epilogue(const Args& a, int64_t i, int64
 // ---------------------------------------------------------------- kernel
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
-    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Args a) {
+    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmG, const Args a) {
   using C = Cfg<CG>;
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
   constexpr int S = C::STAGES;
@@ -438,9 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     uint32_t it = 0;
     bool ok = true;
+    const uint32_t bytes = C::A_BYTES * CG + (uint32_t)a.bn * BK * 2;
     for (int t = first; t < plan.tiles && ok; t += step) {
       const Tile tile = plan.at(t);
-      const int row_a = tile.m * BM * CG + rank * BM + a.a_row, row_b = tile.n * BN + rank * C::B_ROWS + a.b_row;
+      const int row_a = tile.m * BM * CG + rank * BM + a.a_row, row_b = tile.n * a.bn + rank * (a.bn / CG) + a.b_row;
       for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {
         const int term = a.terms == 1 ? 5 : kb / plan.kb;
         const int k = (a.terms == 1 ? kb : kb - term * plan.kb) * BK;
@@ -454,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
         uint32_t bar = full + 8 * s;
-        if (rank == 0) mbar_arrive_expect_tx(bar, C::STAGE * CG);
+        if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
         if constexpr (CG == 2) bar = in_leader(bar);
         load_tile<CG, BM, A_MN>(sa, &tmA, bar, row_a, k + a.a_k, plane_a);
         load_tile<CG, C::B_ROWS, B_MN>(sb, &tmB, bar, row_b, k + a.b_k, plane_b);
@@ -464,39 +492,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t i = it > S ? it - S : 0; i < it; ++i) mbar_wait(full + 8 * (i % S), (i / S) & 1u);
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
-    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
-                               ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM * CG >> 4) << 24);
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
+                           ((uint32_t)(a.bn >> 3) << 17) | ((uint32_t)(BM * CG >> 4) << 24);
     uint32_t it = 0, n_acc = 0;
     bool ok = true;
     for (int t = first; t < plan.tiles && ok; t += step) {
       const Tile tile = plan.at(t);
-      if (tile.kb0 == tile.kb1) continue;
-      const uint32_t as = n_acc & 1u;
-      if (!mbar_wait(acc_empty + 8 * as, ((n_acc >> 1) & 1u) ^ 1u) || *abort_flag) {
-        *abort_flag = 1;
-        break;
-      }
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t d = tmem + as * BN;
-      for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {
-        const int s = it % S;
-        if (!mbar_wait(full + 8 * s, (it / S) & 1u) || *abort_flag) {
+      for (int c0 = tile.kb0, c1; c0 < tile.kb1 && ok; c0 = c1, ++n_acc) {
+        c1 = plan.chunk_end(a, c0, tile.kb1);
+        const uint32_t as = n_acc & 1u;
+        if (!mbar_wait(acc_empty + 8 * as, ((n_acc >> 1) & 1u) ^ 1u) || *abort_flag) {
           *abort_flag = 1;
           ok = false;
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
+        const uint32_t d = tmem + as * BN;
+        for (int kb = c0; kb < c1; ++kb, ++it) {
+          const int s = it % S;
+          if (!mbar_wait(full + 8 * s, (it / S) & 1u) || *abort_flag) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t da = A_MN ? sdesc(sa + kk * 2048, 8192) : sdesc(sa + kk * 32, 16);
-          const uint64_t db = B_MN ? sdesc(sb + kk * 2048, 8192) : sdesc(sb + kk * 32, 16);
-          mma<CG>(d, da, db, idesc, kb > tile.kb0 || kk > 0);
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t da = A_MN ? sdesc(sa + kk * 2048, 8192) : sdesc(sa + kk * 32, 16);
+            const uint64_t db = B_MN ? sdesc(sb + kk * 2048, 8192) : sdesc(sb + kk * 32, 16);
+            mma<CG>(d, da, db, idesc, kb > c0 || kk > 0);
+          }
+          commit<CG>(empty + 8 * s);
         }
-        commit<CG>(empty + 8 * s);
+        if (ok) commit<CG>(acc_full + 8 * as);
       }
-      if (ok) commit<CG>(acc_full + 8 * as);
-      ++n_acc;
     }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
@@ -508,42 +538,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t i = (int64_t)tile.m * BM * CG + rank * BM + q * 32 + lane;
       bool on = i < M;
       const int64_t n = on && a.row_of ? a.row_of[i] : i;
-      const int v0 = tile.n * BN + half * 128 + a.b_row;
+      const int v0 = tile.n * a.bn + half * 128 + a.b_row;
       int pos = 0;
-      if constexpr (KIND == STATS || KIND == GRAD) {
+      if constexpr (KIND == STATS || KIND == GRAD || KIND == GRAD3) {
         if (on && a.list.K > 1) pos = lower_bound(a.list.ids + n * a.list.K, a.list.K, v0);
       }
-      const bool any = tile.kb0 < tile.kb1;
-      const uint32_t as = n_acc & 1u;
-      if (any) {
+      float x[4][32];
+      bool ok = true;
+      if (tile.kb0 == tile.kb1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[c][j] = 0.f;
+      }
+      for (int c0 = tile.kb0; c0 < tile.kb1; c0 = plan.chunk_end(a, c0, tile.kb1), ++n_acc) {
+        const uint32_t as = n_acc & 1u;
         if (!mbar_wait(acc_full + 8 * as, (n_acc >> 1) & 1u) || *abort_flag) {
           *abort_flag = 1;
+          ok = false;
           break;
         }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      }
-      const uint32_t d = tmem + as * BN + lanes + half * 128;
-      auto acc = [&](int c, float* v) {
         __syncwarp();
-        if (any) {
-          ld32(d + c, v);
-        } else {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t d = tmem + as * BN + lanes + half * 128;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        for (int c = 0; c < 8; ++c) {
+          float v[16];
+          ld16(d + c * 16, v);
+          if (c0 == tile.kb0) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[c >> 1][(c & 1) * 16 + j] = v[j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[c >> 1][(c & 1) * 16 + j] += v[j];
+          }
         }
-      };
-      if constexpr (KIND == STATS) stats_epilogue(a, i, n, on, tile.n, half, v0, pos, acc);
-      else if constexpr (KIND == GRAD) grad_epilogue(a, i, n, on, tile.n, half, v0, pos, acc);
-      else product_epilogue(a, i, n, on, tile.n, half, tile.split, acc);
-      if (any) {
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 1) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(acc_empty + 8 * as) : "memory");
           else arrive_at(in_leader(acc_empty + 8 * as));
         }
-        ++n_acc;
       }
+      if (!ok) break;
+      if constexpr (KIND == STATS) stats_epilogue(a, i, n, on, tile.n, half, v0, pos, x);
+      else if constexpr (KIND == GRAD || KIND == GRAD3)
+        grad_epilogue<KIND == GRAD ? 1 : 3>(a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n,
+                                            on, tile.n, half, v0, pos, x);
+      else product_epilogue(a, i, n, on, tile.n, half, tile.split, x);
+    }
+    if constexpr (KIND == GRAD || KIND == GRAD3) {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
   __syncwarp();
