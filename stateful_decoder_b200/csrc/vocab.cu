@@ -15,6 +15,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "vocab.h"
 #include "vocab_gemm.cuh"
@@ -94,54 +95,8 @@ __global__ void __launch_bounds__(128) teacher_prep_kernel(const int32_t* ids, c
 }
 
 // ------------------------------------------------------------------ rows
-// The rows that take part, in order: row_of[i] -> n, pos_of[n] -> i (or -1),
-// and their count.  Forward (weight null) also writes the zeros of the others.
-__global__ void __launch_bounds__(1024) rows_kernel(RowList list, const float* weight, int N, int V, int32_t* row_of,
-                                                    int32_t* pos_of, int32_t* count, float* loss, float* lse) {
-  griddep_enter();
-  __shared__ int warp_sum_s[32];
-  __shared__ int base_s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) base_s = 0;
-  __syncthreads();
-  for (int64_t n0 = 0; n0 < N; n0 += 1024) {
-    const int64_t n = n0 + threadIdx.x;
-    const bool on = n < N && takes_part(list, n, V) && (weight == nullptr || weight[n] != 0.f);
-    const unsigned b = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) warp_sum_s[warp] = __popc(b);
-    __syncthreads();
-    const int base = base_s;
-    int mine = lane < 32 ? warp_sum_s[lane] : 0;
-    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
-    const int total = __reduce_add_sync(0xffffffffu, mine);
-    const int at = base + before + __popc(b & ((1u << lane) - 1));
-    if (n < N) {
-      pos_of[n] = on ? at : -1;
-      if (on) row_of[at] = (int32_t)n;
-      else if (loss) {
-        loss[n] = 0.f;
-        lse[n] = 0.f;
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) base_s = base + total;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) *count = base_s;
-}
-
-// 8 elements from column c of a row (zeros past d).
-template <typename T>
-__device__ __forceinline__ void row8(const T* row, int c, int d, bool vec, float* v) {
-  if (vec && c + 8 <= d) {
-    load8(row + c, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < d ? to_f32(row[c + j]) : 0.f;
-  }
-}
-// The bf16 planes of 8 elements: x0 = bf16(x), x1 = bf16(x - x0), ...; their
-// sum is x to 24 bits.
+// The bf16 planes of 8 elements: x0 = bf16(x), x1 = bf16(x - x0), ...; the sum
+// of three is x to 24 bits.
 __device__ __forceinline__ void planes8(bf16* dst, int64_t plane, int planes, float* v) {
   for (int p = 0; p < planes; ++p) {
     store8(dst + p * plane, v);
@@ -149,113 +104,403 @@ __device__ __forceinline__ void planes8(bf16* dst, int64_t plane, int planes, fl
     for (int j = 0; j < 8; ++j) v[j] -= to_f32(from_f32<bf16>(v[j]));
   }
 }
-
-// One warp per row.  out row pos_of[n] (or n) = h row n as bf16 planes; rows
-// that take no part get a zero dh row instead; the 128 warps behind the last
-// row write zero rows up to the next multiple of 128.
+// One row by a warp, four groups of eight in flight per lane.
 template <typename T>
-__global__ void __launch_bounds__(256) gather_kernel(const T* x, int64_t ld, int64_t rows, int d, int vec,
-                                                     const int32_t* pos_of, const int32_t* count, bf16* out,
-                                                     int64_t ld_out, int64_t plane, int planes, T* zero,
-                                                     int64_t ld_zero) {
-  griddep_enter();
-  const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+__device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out, int64_t plane, int planes) {
   const int lane = threadIdx.x & 31;
-  if (n < rows) {
-    const int64_t i = pos_of ? pos_of[n] : n;
-    if (i < 0) {
-      if (zero)
-        for (int c = lane; c < d; c += 32) zero[n * ld_zero + c] = from_f32<T>(0.f);
-      return;
+  for (int c0 = lane * 8; c0 < d; c0 += 1024) {
+    float v[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + u * 256;
+      if (vec && c + 8 <= d) {
+        load8(x + c, v[u]);
+      } else if (c < d) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[u][j] = c + j < d ? to_f32(x[c + j]) : 0.f;
+      }
     }
-    for (int c = lane * 8; c < d; c += 256) {
-      float v[8];
-      row8(x + n * ld, c, d, vec, v);
-      planes8(out + i * ld_out + c, plane, planes, v);
-    }
-  } else if (count && n < rows + 128) {
-    const int64_t i = *count + (n - rows);
-    if (i >= (*count + 127) / 128 * 128) return;
-    for (int c = lane * 8; c < d; c += 256) {
-      float v[8] = {};
-      planes8(out + i * ld_out + c, plane, planes, v);
-    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (c0 + u * 256 < d) planes8(out + c0 + u * 256, plane, planes, v[u]);
   }
 }
 
-// Joins the statistics of a row's column groups; the row's loss.  A block has
-// 32 rows (x) by 32 groups of column groups (y); the order is fixed.
+struct Gather {
+  // rows of h that take part, in order, to `h_out`; row_of[i] -> row
+  RowList list;
+  const float* weight;  // backward: rows of weight 0 are left out too
+  int N, V, d;
+  int row_blocks, rows_per_block, pad_blocks;  // 0: h is read where it is
+  const void* h;
+  int64_t ld_h;
+  int vec_h;
+  bf16* h_out;
+  int64_t h_plane;
+  int32_t* row_of;
+  int32_t* count;
+  float *loss, *lse;    // forward: zeros for the others
+  void* dh;             // backward: a zero row for the others
+  int64_t ld_dh;
+  // rows of w to `w_out`
+  int w_blocks;
+  const void* w;
+  int64_t ld_w;
+  int vec_w;
+  bf16* w_out;
+  int64_t w_plane;
+  int64_t ld_out;
+  int planes;
+};
+
+__device__ __forceinline__ int count_rows(const Gather& g, int64_t end, int* red) {
+  int n_on = 0;
+#pragma unroll 8
+  for (int64_t n = threadIdx.x; n < end; n += 256)
+    n_on += takes_part(g.list, n, g.V) && (g.weight == nullptr || g.weight[n] != 0.f);
+  n_on = __reduce_add_sync(0xffffffffu, n_on);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n_on;
+  __syncthreads();
+  int r = 0;
+  for (int i = 0; i < 8; ++i) r += red[i];
+  __syncthreads();
+  return r;
+}
+
+// Operands of the contractions in one launch: blocks that gather rows of h
+// (each counts the rows before its own), blocks that zero the rows behind the
+// last one up to a multiple of 128, blocks that convert w.
+template <typename T>
+__global__ void __launch_bounds__(256) gather_kernel(const Gather g) {
+  griddep_enter();
+  __shared__ int red[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int b = (int)blockIdx.x;
+  if (b < g.row_blocks) {
+    const int64_t n0 = (int64_t)b * g.rows_per_block;
+    int at = count_rows(g, min((int64_t)g.N, n0), red);
+    for (int64_t r = n0; r < min((int64_t)g.N, n0 + g.rows_per_block); r += 8) {
+      const int64_t n = r + warp;
+      const bool on = n < g.N && takes_part(g.list, n, g.V) && (g.weight == nullptr || g.weight[n] != 0.f);
+      if (lane == 0) red[warp] = on;
+      __syncthreads();
+      int before = 0, all = 0;
+      for (int i = 0; i < 8; ++i) {
+        before += i < warp ? red[i] : 0;
+        all += red[i];
+      }
+      __syncthreads();
+      const int64_t i = at + before;
+      at += all;
+      if (on) {
+        if (lane == 0) g.row_of[i] = (int32_t)n;
+        copy_row(static_cast<const T*>(g.h) + n * g.ld_h, g.d, g.vec_h, g.h_out + i * g.ld_out, g.h_plane, g.planes);
+      } else if (n < g.N) {
+        if (g.loss && lane == 0) {
+          g.loss[n] = 0.f;
+          g.lse[n] = 0.f;
+        }
+        if (g.dh)
+          for (int c = lane; c < g.d; c += 32) static_cast<T*>(g.dh)[n * g.ld_dh + c] = from_f32<T>(0.f);
+      }
+    }
+    return;
+  }
+  b -= g.row_blocks;
+  if (b < g.pad_blocks) {
+    const int count = count_rows(g, g.N, red);
+    if (b == 0 && threadIdx.x == 0) *g.count = count;
+    const int64_t i = (int64_t)count + b * 8 + warp;
+    if (i >= (count + 127) / 128 * 128) return;
+    for (int c = lane * 8; c < g.d; c += 256) {
+      float v[8] = {};
+      planes8(g.h_out + i * g.ld_out + c, g.h_plane, g.planes, v);
+    }
+    return;
+  }
+  b -= g.pad_blocks;
+  const int64_t v = (int64_t)b * 8 + warp;
+  if (v < g.V)
+    copy_row(static_cast<const T*>(g.w) + v * g.ld_w, g.d, g.vec_w, g.w_out + v * g.ld_out, g.w_plane, g.planes);
+}
+
+// Joins the statistics of a row's column groups, in a fixed order, and writes
+// the row's loss.  A block has 32 rows; first lane = row and warp = group,
+// then warp = row and lane = group.
 __global__ void __launch_bounds__(1024) join_kernel(const float2* part, int parts, int64_t ld, int N,
                                                     const int32_t* row_of, const int32_t* count, int V, RowList list,
                                                     const float* slogq, const float* zsel, float* loss, float* lse) {
   griddep_enter();
   __shared__ float ms[32][33], ss[32][33];
-  const int x = threadIdx.x, y = threadIdx.y;
-  const int64_t i = (int64_t)blockIdx.x * 32 + x;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rows = count ? *count : N;
-  const bool in = i < rows;
-  float m = -INFINITY, s = 0.f;
-  if (in) {
-    for (int t = y; t < parts; t += 32) {
-      const float2 p = part[(int64_t)t * ld + i];
-      const float mn = fmaxf(m, p.x);
-      const float a = m > -INFINITY ? expf(m - mn) : (isnan(s) ? s : 0.f);
-      const float b = p.x > -INFINITY ? expf(p.x - mn) : (isnan(p.y) ? p.y : 0.f);
-      s = s * a + p.y * b;
-      m = mn;
+  if ((int64_t)blockIdx.x * 32 >= rows) return;
+  {
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.f;
+    if (i < rows) {
+      for (int t0 = w; t0 < parts; t0 += 256) {
+        float2 p[8];
+        float mn = m;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          p[u] = t0 + u * 32 < parts ? part[(int64_t)(t0 + u * 32) * ld + i] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mn = fmaxf(mn, p[u].x);
+        const float ref = mn > -INFINITY ? mn : 0.f;
+        s = s == 0.f ? 0.f : s * expf(m - ref);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += p[u].y == 0.f ? 0.f : p[u].y * expf(p[u].x - ref);
+        m = mn;
+      }
     }
+    ms[w][lane] = m;
+    ss[w][lane] = s;
   }
-  ms[y][x] = m;
-  ss[y][x] = s;
   __syncthreads();
-  const int64_t n = in && row_of ? row_of[i] : i;
-  const bool on = in && (row_of || takes_part(list, n, V));
-  float M = -INFINITY, total = 0.f;
-  for (int j = 0; j < 32; ++j) M = fmaxf(M, ms[j][x]);
-  for (int j = 0; j < 32; ++j) {
-    const float mj = ms[j][x], sj = ss[j][x];
-    total += mj > -INFINITY ? sj * expf(mj - M) : (isnan(sj) ? sj : 0.f);
-  }
-  const float l = M + logf(total);
-  if (list.q == nullptr) {
-    if (y == 0 && in) {
-      lse[n] = on ? l : 0.f;
-      loss[n] = on ? zsel[n] - l : 0.f;
+  const int64_t i = (int64_t)blockIdx.x * 32 + w;
+  if (i >= rows) return;
+  const int64_t n = row_of ? row_of[i] : i;
+  if (!row_of && !takes_part(list, n, V)) {
+    if (lane == 0) {
+      loss[n] = 0.f;
+      lse[n] = 0.f;
     }
     return;
   }
-  float kl = 0.f;
-  if (on)
-    for (int k = y; k < list.K; k += 32) {
+  const float m = ms[lane][w], s = ss[lane][w];
+  const float M = warp_max(m), ref = M > -INFINITY ? M : 0.f;
+  const float l = M + logf(warp_sum(s == 0.f ? 0.f : s * expf(m - ref)));
+  float r = 0.f;
+  if (list.q == nullptr) {
+    r = zsel[n] - l;
+  } else {
+    for (int k = lane; k < list.K; k += 32) {
       const int64_t e = n * list.K + k;
-      if (list.ids[e] != kNoId && list.q[e] != 0.f) kl += list.q[e] * (slogq[e] - zsel[e] + l);
+      if (list.ids[e] != kNoId && list.q[e] != 0.f) r += list.q[e] * (slogq[e] - zsel[e] + l);
     }
-  __syncthreads();
-  ss[y][x] = kl;
-  __syncthreads();
-  if (y == 0 && in) {
-    float r = 0.f;
-    for (int j = 0; j < 32; ++j) r += ss[j][x];
-    lse[n] = on ? l : 0.f;
-    loss[n] = on ? r : 0.f;
+    r = warp_sum(r);
+  }
+  if (lane == 0) {
+    lse[n] = l;
+    loss[n] = r;
   }
 }
 
-// out rows = the slabs' sum in order (a long K split over the SMs).
+// out rows of the tiles whose K was split = the slabs' sum in order.
+struct SlabSum {
+  const float* slab;
+  int M, N, K;
+  const int32_t *m_count, *k_count;
+  int terms, units, max_splits, cg;
+  const int32_t* row_of;
+  void* out;
+  int64_t ld;
+  int accumulate, vec;
+  float* acc;  // as in Args
+  int acc_in, acc_out;
+};
 template <typename T>
-__global__ void __launch_bounds__(256) slab_sum_kernel(const float* slab, int splits, int64_t slab_rows, int rows,
-                                                       const int32_t* count, int d, const int32_t* row_of, T* out,
-                                                       int64_t ld, int accumulate) {
+__global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
   griddep_enter();
-  const int64_t i = blockIdx.y;
-  if (i >= (count ? *count : rows)) return;
-  const int64_t n = row_of ? row_of[i] : i;
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= d) return;
-  float s = 0.f;
-  for (int k = 0; k < splits; ++k) s += slab[((int64_t)k * slab_rows + i) * d + c];
-  T* o = out + n * ld + c;
-  *o = from_f32<T>(accumulate ? s + to_f32(*o) : s);
+  const int M = a.m_count ? *a.m_count : a.M, K = a.k_count ? *a.k_count : a.K;
+  const int tile_rows = BM * a.cg;
+  Cut cut;
+  cut.init(M, a.N, K, tile_rows, BN, a.terms, a.units, a.max_splits);
+  const int total = cut.rest * tile_rows * (BN / 8);
+  const int64_t stride = (int64_t)cut.rest * tile_rows * BN;
+  for (int e = (int)blockIdx.x * 256 + threadIdx.x; e < total; e += (int)gridDim.x * 256) {
+    const int c = e % (BN / 8) * 8, row = e / (BN / 8);
+    int m, nt;
+    cut.place(cut.whole + row / tile_rows, kPanel / a.cg, &m, &nt);
+    const int64_t i = (int64_t)m * tile_rows + row % tile_rows;
+    const int col = nt * BN + c;
+    if (i >= M || col >= a.N) continue;
+    float s[8] = {};
+    for (int k = 0; k < cut.splits; ++k) {
+      float v[8];
+      load8(a.slab + k * stride + (int64_t)row * BN + c, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += v[j];
+    }
+    if (a.acc) {
+      float* p = a.acc + i * a.N + col;
+      const int cols = min(8, a.N - col);
+      if (a.acc_in)
+        for (int j = 0; j < cols; ++j) s[j] += p[j];
+      if (a.acc_out) {
+        for (int j = 0; j < cols; ++j) p[j] = s[j];
+        continue;
+      }
+    }
+    T* o = static_cast<T*>(a.out) + (a.row_of ? a.row_of[i] : i) * a.ld + col;
+    if (a.vec && col + 8 <= a.N) {
+      if (a.accumulate) {
+        float old[8];
+        load8(o, old);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += old[j];
+      }
+      store8(o, s);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < a.N) o[j] = from_f32<T>(a.accumulate ? s[j] + to_f32(o[j]) : s[j]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ few rows
+// Statistics of up to 8 rows: bound by reading w once, so w goes through
+// registers and h through shared memory, in fp32.  A warp takes R rows of w at
+// a time (16-byte loads, 256 columns per step) against all NB rows of h; the
+// R x NB sums of its lanes are added by exchanging halves, after which lane
+// r * NB + n holds z of w row r and h row n.
+// At V = 32000, d = 2048, one row: see the table of DESIGN for its time
+// against the tensor-core path, which reads w at 4.1 TB/s here (every SM asks
+// for the same 128 bytes of h at a time).
+template <typename T, int NB>
+struct FewCfg {
+  static constexpr int R = NB == 8 ? 4 : 8;
+  static constexpr int WARPS = 16;
+};
+constexpr int kFewRows = 8;
+constexpr size_t kFewSmem = 200 << 10;  // h in shared memory
+
+template <typename T>
+struct Raw;
+template <>
+struct Raw<bf16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const bf16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t w = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w;
+    return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+  }
+  __device__ __forceinline__ float get(int j) const {
+    const float4& v = j < 4 ? a : b;
+    return (j & 3) == 0 ? v.x : (j & 3) == 1 ? v.y : (j & 3) == 2 ? v.z : v.w;
+  }
+};
+
+template <typename T, int NB>
+__global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld_h, const T* w, int64_t ld_w, int N,
+                                                          int V, int d, int vec, float scale, RowList list,
+                                                          float2* part, int64_t part_ld, float* zsel) {
+  constexpr int R = FewCfg<T, NB>::R;
+  extern __shared__ float4 hs[];  // [NB][2][d8]: the two halves of every group of eight
+  __shared__ float2 sums[16][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d8 = (d + 7) / 8;
+  griddep_enter();
+  for (int i = threadIdx.x; i < NB * d8 * 2; i += 512) {
+    const int n = i / (d8 * 2), r = i - n * d8 * 2, half = r / d8, g = r - half * d8;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = g * 8 + half * 4 + j;
+      v[j] = n < N && k < d ? to_f32(h[n * ld_h + k]) : 0.f;
+    }
+    hs[i] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  __syncthreads();
+  const int n = lane % NB, r = lane / NB;  // what this lane finishes
+  const bool mine = lane < R * NB && n < N;
+  int pos = 0, next = mine ? list.ids[(int64_t)n * list.K] : kNoId;
+  float m = -INFINITY, s = 0.f;
+  const int groups = (V + R - 1) / R, step = (int)gridDim.x * 16;
+  for (int g = warp * (int)gridDim.x + (int)blockIdx.x; g < groups; g += step) {
+    float acc[R * NB];
+#pragma unroll
+    for (int i = 0; i < R * NB; ++i) acc[i] = 0.f;
+    const int64_t v0 = (int64_t)g * R;
+    for (int c = lane; c < d8; c += 32) {
+      Raw<T> x[R];
+      if (vec && c * 8 + 8 <= d) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[i].load(w + min(v0 + i, (int64_t)V - 1) * ld_w + c * 8);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float4 lo = hs[(b * 2) * d8 + c], hi = hs[(b * 2 + 1) * d8 + c];
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            float& t = acc[i * NB + b];
+            t = fmaf(x[i].get(0), lo.x, t);
+            t = fmaf(x[i].get(1), lo.y, t);
+            t = fmaf(x[i].get(2), lo.z, t);
+            t = fmaf(x[i].get(3), lo.w, t);
+            t = fmaf(x[i].get(4), hi.x, t);
+            t = fmaf(x[i].get(5), hi.y, t);
+            t = fmaf(x[i].get(6), hi.z, t);
+            t = fmaf(x[i].get(7), hi.w, t);
+          }
+        }
+      } else {
+        const float* hf = reinterpret_cast<const float*>(hs);
+        for (int j = 0; j < 8 && c * 8 + j < d; ++j) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float y = to_f32(w[min(v0 + i, (int64_t)V - 1) * ld_w + c * 8 + j]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              acc[i * NB + b] = fmaf(y, hf[((b * 2 + (j >> 2)) * d8 + c) * 4 + (j & 3)], acc[i * NB + b]);
+          }
+        }
+      }
+    }
+    // sums over the lanes: value i ends in lane i (values beyond 32 lanes' worth of halvings stay whole)
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+      if (off >= R * NB) {
+#pragma unroll
+        for (int i = 0; i < R * NB; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+      } else {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < R * NB; ++i) {
+          if (i < off) {
+            const float send = upper ? acc[i] : acc[i + off], keep = upper ? acc[i + off] : acc[i];
+            acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+          }
+        }
+      }
+    }
+    const int64_t v = v0 + r;
+    if (mine && v < V) {
+      const float z = acc[0] * scale;
+      while (next < v && pos + 1 < list.K) next = list.ids[(int64_t)n * list.K + ++pos];
+      while (next == v) {
+        zsel[(int64_t)n * list.K + pos] = z;
+        next = ++pos < list.K ? list.ids[(int64_t)n * list.K + pos] : kNoId;
+      }
+      const float mn = fmaxf(m, z), ref = mn > -INFINITY ? mn : 0.f;
+      s = (s == 0.f ? 0.f : s * expf(m - ref)) + expf(z - ref);
+      m = mn;
+    }
+  }
+  sums[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp == 0 && lane < NB && lane < N) {  // the block's statistics of row `lane`
+    float M = -INFINITY, total = 0.f;
+    for (int k = 0; k < 16; ++k)
+      for (int i = 0; i < R; ++i) M = fmaxf(M, sums[k][i * NB + lane].x);
+    const float ref = M > -INFINITY ? M : 0.f;
+    for (int k = 0; k < 16; ++k)
+      for (int i = 0; i < R; ++i) {
+        const float2 t = sums[k][i * NB + lane];
+        total += t.y == 0.f ? 0.f : t.y * expf(t.x - ref);
+      }
+    part[(int64_t)blockIdx.x * part_ld + lane] = make_float2(M, total);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -301,6 +546,19 @@ cudaError_t tensor_map(CUtensorMap* tm, const Matrix& m, int box_rows, int box_c
     if (e_ != cudaSuccess) return e_; \
   } while (0)
 
+// Raises a kernel's shared-memory limit, once per device.
+template <auto Kernel>
+cudaError_t set_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  VOCAB_TRY(cudaGetDevice(&dev));
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  VOCAB_TRY(cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 template <int KIND, int CG>
 cudaError_t launch(const Matrix& A, const Matrix& B, const Matrix* G, const Args& a, cudaStream_t st) {
   using C = Cfg<CG>;
@@ -310,8 +568,8 @@ cudaError_t launch(const Matrix& A, const Matrix& B, const Matrix* G, const Args
   VOCAB_TRY(tensor_map(&tb, B, B_MN ? 64 : a.bn / CG));
   if (G) VOCAB_TRY(tensor_map(&tg, *G, 32, 32));
   else tg = ta;
-  VOCAB_TRY(cudaFuncSetAttribute(vocab_gemm_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-  const int64_t tiles = round_up(a.M, BM * CG) / (BM * CG) * (round_up(a.N, a.bn) / a.bn) * a.splits;
+  VOCAB_TRY((set_smem<vocab_gemm_kernel<KIND, CG>>(C::SMEM)));
+  const int64_t tiles = round_up(a.M, BM * CG) / (BM * CG) * (round_up(a.N, a.bn) / a.bn) * a.max_splits;
   if (tiles == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, kSmCount / CG) * CG));
@@ -341,23 +599,33 @@ cudaError_t contract(const Matrix& A, const Matrix& B, const Matrix* G, const Ar
 
 // Where things lie in the workspace, and how the work is cut.
 struct Layout {
-  size_t sid = 0, sq = 0, slogq = 0, some = 0, row_of = 0, pos_of = 0, count = 0, h = 0, w = 0, part = 0, zsel = 0,
-         g = 0, dh = 0, dw = 0, total = 0;
-  int planes = 1, terms = 1;
-  bool gather = true, pack_w = false;
+  size_t sid = 0, sq = 0, slogq = 0, some = 0, row_of = 0, count = 0, h = 0, w = 0, part = 0, zsel = 0, g = 0,
+         dh = 0, dw = 0, acc = 0, total = 0;
+  int planes = 1, terms = 1;      // of h and w, and of h w^T
+  int g_planes = 1, g_terms = 1;  // of g, and of its products
+  bool few = false, gather = true, pack_w = false;
   int64_t rows = 0;  // rows of the gathered operand, a multiple of 256
   int64_t ld = 0;    // row distance of gathered and packed operands
-  int bn = BN, n_tiles = 0, piece = 0, pieces = 0, dh_splits = 1, dw_splits = 1;
-  bool dh_slab = false;
+  int bn = BN, parts = 0, piece = 0, pieces = 0;
+  int dh_splits = 1, dw_splits = 1;  // at most
 };
 
 bool tma_ready(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
 
-// Splits of a long K for a product with too few tiles to fill the SMs, at
-// least eight k-blocks each.
-int split_count(int64_t tiles, int64_t kblocks) {
-  if (tiles * 2 > kSmCount) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(kSmCount / tiles, kblocks / 8));
+constexpr int kMostSplits = 16;
+int cta_group(int M) { return M > BM ? 2 : 1; }
+// Floats that the split sums of a product can take: split_rule makes at most
+// two rounds of split tiles, and none of fewer than 32 k-blocks.
+int64_t slab_floats(int64_t M, int64_t N, int64_t kblocks, int* most) {
+  *most = kblocks >= 32 ? kMostSplits : 1;
+  if (*most == 1) return 0;
+  const int64_t n_tiles = (N + BN - 1) / BN;
+  int64_t need = 0;
+  for (int cg = 1; cg <= 2; ++cg) {
+    const int64_t all = (M + BM * cg - 1) / (BM * cg) * n_tiles;
+    need = std::max(need, std::min<int64_t>(2 * (kSmCount / cg), all * kMostSplits) * BM * cg * BN);
+  }
+  return need;
 }
 
 Layout layout(const VocabLoss& p, int backward) {
@@ -372,18 +640,6 @@ Layout layout(const VocabLoss& p, int backward) {
   L.terms = f32 ? 6 : 1;
   L.rows = round_up(std::max(p.N, 1), 256);
   L.ld = round_up(p.d, 8);
-  // A forward pass over one row tile has nothing to gain from leaving rows
-  // out, and its rows do not mix: it reads h where it is.
-  L.gather = f32 || backward || p.N > BM || !tma_ready(p.h, p.ld_h);
-  L.pack_w = f32 || !tma_ready(p.w, p.ld_w);
-  L.n_tiles = (p.V + BN - 1) / BN;
-  if (!backward && p.N <= BM) {
-    // One row tile: the work is reading w once.  Columns per tile so that the
-    // tiles fill whole rounds of the SMs evenly.
-    const int rounds = (L.n_tiles + kSmCount - 1) / kSmCount;
-    L.bn = std::max(32, (int)round_up((p.V + kSmCount * rounds - 1) / (kSmCount * rounds), 16));
-    L.n_tiles = (p.V + L.bn - 1) / L.bn;
-  }
   const size_t n = (size_t)p.N;
   if (p.teacher) {
     L.sid = take(n * p.K * 4);
@@ -391,31 +647,49 @@ Layout layout(const VocabLoss& p, int backward) {
     L.slogq = take(n * p.K * 4);
     L.some = take(n * 4);
   }
+  L.few = !backward && p.N <= kFewRows && (size_t)kFewRows * round_up(p.d, 8) * 4 <= kFewSmem;
+  // A forward pass over one row tile has nothing to gain from leaving rows
+  // out, and its rows do not mix: it reads h where it is.
+  L.gather = !L.few && (f32 || backward || p.N > BM || !tma_ready(p.h, p.ld_h));
+  L.pack_w = !L.few && (f32 || !tma_ready(p.w, p.ld_w));
   if (L.gather) {
     L.row_of = take(n * 4);
-    L.pos_of = take(n * 4);
     L.count = take(4);
     L.h = take((size_t)L.planes * L.rows * L.ld * 2);
   }
   if (L.pack_w) L.w = take((size_t)L.planes * p.V * L.ld * 2);
+  const int64_t n_tiles = (p.V + BN - 1) / BN;
   if (!backward) {
-    L.part = take((size_t)2 * L.n_tiles * L.rows * 8);
+    L.parts = (int)(2 * n_tiles);
+    if (L.few) {
+      L.parts = (int)std::min<int64_t>(kSmCount, (p.V + 15) / 16);
+    } else if (p.N <= BM) {
+      // One row tile: the work is reading w once.  Columns per tile so that
+      // the tiles fill whole rounds of the SMs evenly.
+      const int64_t rounds = (n_tiles + kSmCount - 1) / kSmCount;
+      L.bn = std::max(32, (int)round_up((p.V + kSmCount * rounds - 1) / (kSmCount * rounds), 16));
+      L.parts = 2 * ((p.V + L.bn - 1) / L.bn);
+    }
+    L.part = take((size_t)L.parts * (L.few ? kFewRows : L.rows) * 8);
     L.zsel = take(n * p.K * 4);
     return L;
   }
+  // g of bf16 operands is rounded to bf16 as an operand of the products, about
+  // as much again as the gradients' own rounding.  Up to 256 rows a second
+  // plane costs next to nothing (the products are bound by w and dw) and
+  // leaves their own rounding alone.
+  L.g_planes = f32 ? 3 : p.N <= 256 ? 2 : 1;
+  L.g_terms = f32 ? 6 : L.g_planes;
   // The piece: as wide as 512 MB of g allow, at least 2048 columns; equal pieces.
-  const int64_t most = std::max<int64_t>(2048, ((int64_t)512 << 20) / (L.rows * 2 * L.planes) / BN * BN);
-  const int64_t whole = (int64_t)L.n_tiles * BN;
+  const int64_t most = std::max<int64_t>(2048, ((int64_t)512 << 20) / (L.rows * 2 * L.g_planes) / BN * BN);
+  const int64_t whole = n_tiles * BN;
   L.pieces = (int)((whole + most - 1) / most);
   L.piece = (int)round_up((whole + L.pieces - 1) / L.pieces, BN);
   L.pieces = (int)((whole + L.piece - 1) / L.piece);
-  L.g = take((size_t)L.planes * L.rows * L.piece * 2);
-  const int64_t dt = (p.d + BN - 1) / BN;
-  L.dh_splits = split_count(L.rows / BM * dt, (int64_t)L.piece / BK * L.terms);
-  L.dh_slab = L.dh_splits > 1 || L.pieces > 1;
-  if (L.dh_slab) L.dh = take((size_t)L.dh_splits * L.rows * p.d * 4);
-  L.dw_splits = split_count(L.piece / BM * dt, (int64_t)L.rows / BK * L.terms);
-  if (L.dw_splits > 1) L.dw = take((size_t)L.dw_splits * L.piece * p.d * 4);
+  L.g = take((size_t)L.g_planes * L.rows * L.piece * 2);
+  L.dw = take((size_t)slab_floats(L.piece, p.d, L.rows / BK * L.g_terms, &L.dw_splits) * 4);
+  L.dh = take((size_t)slab_floats(p.N, p.d, (int64_t)L.piece / BK * L.g_terms, &L.dh_splits) * 4);
+  if (L.pieces > 1) L.acc = take((size_t)L.rows * p.d * 4);  // dh over the pieces
   return L;
 }
 
@@ -432,14 +706,8 @@ struct Prepared {
   Matrix h, w;
 };
 
-template <typename T>
-cudaError_t gather_rows(const void* x, int64_t ld, int64_t rows, int d, const int32_t* pos_of, const int32_t* count,
-                        bf16* out, int64_t ld_out, int64_t plane, int planes, void* zero, int64_t ld_zero,
-                        cudaStream_t st) {
-  const int64_t warps = rows + (count ? 128 : 0);
-  const int vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ld % (16 / (int)sizeof(T)) == 0;
-  return launch_pdl(gather_kernel<T>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, static_cast<const T*>(x),
-                    ld, rows, d, vec, pos_of, count, out, ld_out, plane, planes, static_cast<T*>(zero), ld_zero);
+int vector_rows(const void* p, int64_t ld, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % (dtype ? 8 : 4) == 0;
 }
 
 cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* weight, float* loss, float* lse,
@@ -455,26 +723,47 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
   }
   r->h = Matrix{static_cast<const bf16*>(p.h), p.N, p.d, p.ld_h, 0, 1};
   r->w = Matrix{static_cast<const bf16*>(p.w), p.V, p.d, p.ld_w, 0, 1};
+  if (!L.gather && !L.pack_w) return cudaSuccess;
+  Gather g{};
+  g.N = p.N;
+  g.V = p.V;
+  g.d = p.d;
+  g.ld_out = L.ld;
+  g.planes = L.planes;
   if (L.gather) {
-    int32_t *row_of = at<int32_t>(ws, L.row_of), *pos_of = at<int32_t>(ws, L.pos_of), *count = at<int32_t>(ws, L.count);
-    VOCAB_TRY(launch_pdl(rows_kernel, dim3(1), dim3(1024), 0, st, r->list, weight, p.N, p.V, row_of, pos_of, count,
-                         loss, lse));
-    const int64_t plane = L.rows * L.ld;
-    bf16* h = at<bf16>(ws, L.h);
-    VOCAB_TRY((p.dtype ? gather_rows<bf16> : gather_rows<float>)(p.h, p.ld_h, p.N, p.d, pos_of, count, h, L.ld, plane,
-                                                                 L.planes, dh, ld_dh, st));
-    r->row_of = row_of;
-    r->count = count;
-    r->h = Matrix{h, L.rows, p.d, L.ld, plane, L.planes};
+    g.list = r->list;
+    g.weight = weight;
+    // At most 1024 blocks, each of which counts all rows before its own.
+    g.rows_per_block = (int)round_up((p.N + 1023) / 1024, 8);
+    g.row_blocks = (p.N + g.rows_per_block - 1) / g.rows_per_block;
+    g.pad_blocks = 16;
+    g.h = p.h;
+    g.ld_h = p.ld_h;
+    g.vec_h = vector_rows(p.h, p.ld_h, p.dtype);
+    g.h_out = at<bf16>(ws, L.h);
+    g.h_plane = L.rows * L.ld;
+    g.row_of = at<int32_t>(ws, L.row_of);
+    g.count = at<int32_t>(ws, L.count);
+    g.loss = loss;
+    g.lse = lse;
+    g.dh = dh;
+    g.ld_dh = ld_dh;
+    r->row_of = g.row_of;
+    r->count = g.count;
+    r->h = Matrix{g.h_out, L.rows, p.d, L.ld, g.h_plane, L.planes};
   }
   if (L.pack_w) {
-    const int64_t plane = (int64_t)p.V * L.ld;
-    bf16* w = at<bf16>(ws, L.w);
-    VOCAB_TRY((p.dtype ? gather_rows<bf16> : gather_rows<float>)(p.w, p.ld_w, p.V, p.d, nullptr, nullptr, w, L.ld,
-                                                                 plane, L.planes, nullptr, 0, st));
-    r->w = Matrix{w, p.V, p.d, L.ld, plane, L.planes};
+    g.w_blocks = (p.V + 7) / 8;
+    g.w = p.w;
+    g.ld_w = p.ld_w;
+    g.vec_w = vector_rows(p.w, p.ld_w, p.dtype);
+    g.w_out = at<bf16>(ws, L.w);
+    g.w_plane = (int64_t)p.V * L.ld;
+    r->w = Matrix{g.w_out, p.V, p.d, L.ld, g.w_plane, L.planes};
   }
-  return cudaSuccess;
+  const dim3 grid((unsigned)(g.row_blocks + g.pad_blocks + g.w_blocks));
+  return p.dtype ? launch_pdl(gather_kernel<bf16>, grid, dim3(256), 0, st, g)
+                 : launch_pdl(gather_kernel<float>, grid, dim3(256), 0, st, g);
 }
 
 Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
@@ -482,7 +771,7 @@ Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
   a.terms = L.terms;
   a.chunk = p.dtype ? 16 : 4;
   a.bn = BN;
-  a.splits = 1;
+  a.max_splits = 1;
   a.list = r.list;
   a.row_of = r.row_of;
   a.V = p.V;
@@ -490,20 +779,47 @@ Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
   return a;
 }
 
+template <typename T, int NB>
+cudaError_t few_rows(const VocabLoss& p, const Layout& L, const RowList& list, float2* part, float* zsel,
+                     cudaStream_t st) {
+  const size_t smem = (size_t)NB * round_up(p.d, 8) * 4;
+  VOCAB_TRY((set_smem<few_rows_kernel<T, NB>>((int)kFewSmem)));
+  const int vec = vector_rows(p.w, p.ld_w, p.dtype);
+  return launch_pdl(few_rows_kernel<T, NB>, dim3((unsigned)L.parts), dim3(512), smem, st, static_cast<const T*>(p.h),
+                    p.ld_h, static_cast<const T*>(p.w), p.ld_w, p.N, p.V, p.d, vec, p.inv_t, list, part,
+                    (int64_t)kFewRows, zsel);
+}
 template <typename T>
-cudaError_t slab_sum(const float* slab, int splits, int64_t slab_rows, int rows, const int32_t* count, int d,
-                     const int32_t* row_of, void* out, int64_t ld, int accumulate, cudaStream_t st) {
-  // grid.y is bounded by the slab's own rule: few tiles, so few rows
-  return launch_pdl(slab_sum_kernel<T>, dim3((unsigned)((d + 255) / 256), (unsigned)rows), dim3(256), 0, st, slab,
-                    splits, slab_rows, rows, count, d, row_of, static_cast<T*>(out), ld, accumulate);
+cudaError_t few_rows_of(const VocabLoss& p, const Layout& L, const RowList& list, float2* part, float* zsel,
+                        cudaStream_t st) {
+  if (p.N == 1) return few_rows<T, 1>(p, L, list, part, zsel, st);
+  if (p.N == 2) return few_rows<T, 2>(p, L, list, part, zsel, st);
+  if (p.N <= 4) return few_rows<T, 4>(p, L, list, part, zsel, st);
+  return few_rows<T, 8>(p, L, list, part, zsel, st);
 }
 
-void typed_output(Args* a, void* out, int64_t ld, int dtype, int accumulate) {
-  a->out = out;
-  a->ld_out = ld;
-  a->out_bf16 = dtype;
-  a->accumulate = accumulate;
-  a->vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ld % (dtype ? 8 : 4) == 0;
+// A product of g into typed rows, K split where the rule says so.
+template <int KIND>
+cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a, float* slab, void* out, int64_t ld,
+                    int accumulate, cudaStream_t st) {
+  const int cg = cta_group(a.M);
+  a.units = kSmCount / cg;
+  a.slab = slab;
+  a.out = out;
+  a.ld_out = ld;
+  a.out_bf16 = p.dtype;
+  a.accumulate = accumulate;
+  a.vec = vector_rows(out, ld, p.dtype);
+  // bf16 gradients: a sum's drift over 4096 of k (8e-6) is far below their own rounding
+  if (p.dtype) a.chunk = 64;
+  VOCAB_TRY(contract<KIND>(G, B, nullptr, a, st));
+  if (a.max_splits == 1) return cudaSuccess;
+  const SlabSum s{slab,    a.M,          a.N, a.K,      a.m_count, a.k_count, a.terms,
+                  a.units, a.max_splits, cg,  a.row_of, out,       ld,        accumulate, a.vec,
+                  a.acc,   a.acc_in,     a.acc_out};
+  const dim3 grid((unsigned)std::min<int64_t>(4 * kSmCount, ((int64_t)a.M * a.N + 2047) / 2048));
+  return p.dtype ? launch_pdl(slab_sum_kernel<bf16>, grid, dim3(256), 0, st, s)
+                 : launch_pdl(slab_sum_kernel<float>, grid, dim3(256), 0, st, s);
 }
 
 }  // namespace
@@ -515,19 +831,25 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
   const Layout L = layout(p, 0);
   Prepared r;
   VOCAB_TRY(prepare(p, L, ws, nullptr, loss, lse, nullptr, 0, &r, st));
-  Args a = args_of(p, L, r);
-  a.M = p.N;
-  a.m_count = r.count;
-  a.N = p.V;
-  a.K = p.d;
-  a.part = at<float2>(ws, L.part);
-  a.part_ld = L.rows;
-  a.zsel = at<float>(ws, L.zsel);
-  a.bn = L.bn;
-  VOCAB_TRY(contract<STATS>(r.h, r.w, nullptr, a, st));
-  return launch_pdl(join_kernel, dim3((unsigned)((p.N + 31) / 32)), dim3(32, 32), 0, st, (const float2*)a.part,
-                    2 * L.n_tiles, L.rows, p.N, r.row_of, r.count, p.V, r.list, r.slogq, (const float*)a.zsel, loss,
-                    lse);
+  float2* part = at<float2>(ws, L.part);
+  float* zsel = at<float>(ws, L.zsel);
+  if (L.few) {
+    VOCAB_TRY((p.dtype ? few_rows_of<bf16> : few_rows_of<float>)(p, L, r.list, part, zsel, st));
+  } else {
+    Args a = args_of(p, L, r);
+    a.M = p.N;
+    a.m_count = r.count;
+    a.N = p.V;
+    a.K = p.d;
+    a.bn = L.bn;
+    a.part = part;
+    a.part_ld = L.rows;
+    a.zsel = zsel;
+    VOCAB_TRY(contract<STATS>(r.h, r.w, nullptr, a, st));
+  }
+  return launch_pdl(join_kernel, dim3((unsigned)((p.N + 31) / 32)), dim3(1024), 0, st, (const float2*)part, L.parts,
+                    L.few ? (int64_t)kFewRows : L.rows, p.N, r.row_of, r.count, p.V, r.list, r.slogq,
+                    (const float*)zsel, loss, lse);
 }
 
 cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* weight, void* dh, int64_t ld_dh,
@@ -540,12 +862,10 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
   const Layout L = layout(p, 1);
   Prepared r;
   VOCAB_TRY(prepare(p, L, ws, weight, nullptr, nullptr, dh, ld_dh, &r, st));
-  bf16* g = at<bf16>(ws, L.g);
-  float* slab = L.dh_slab ? at<float>(ws, L.dh) : nullptr;
-  const int64_t g_plane = L.rows * L.piece;
+  float *dh_slab = at<float>(ws, L.dh), *dw_slab = at<float>(ws, L.dw);
+  const Matrix G{at<bf16>(ws, L.g), L.rows, L.piece, L.piece, L.rows * L.piece, L.g_planes};
   for (int i = 0; i < L.pieces; ++i) {
     const int v0 = i * L.piece, width = std::min(p.V - v0, L.piece);
-    const Matrix G{g, L.rows, L.piece, L.piece, g_plane, L.planes};
     Args a = args_of(p, L, r);
     a.M = p.N;
     a.m_count = r.count;
@@ -554,45 +874,33 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.b_row = v0;
     a.lse = lse;
     a.weight = weight;
-    VOCAB_TRY(L.planes == 1 ? contract<GRAD>(r.h, r.w, &G, a, st) : contract<GRAD3>(r.h, r.w, &G, a, st));
+    VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(r.h, r.w, &G, a, st)
+              : L.g_planes == 2 ? contract<GRAD2>(r.h, r.w, &G, a, st)
+                                : contract<GRAD3>(r.h, r.w, &G, a, st));
+    Args b = args_of(p, L, r);
+    b.terms = L.g_terms;
     if (dh) {
-      const bool last = i + 1 == L.pieces;
-      Args b = args_of(p, L, r);
-      // bf16 gradients: the sum's drift over 4096 of k (8e-6) is far below
-      // their own rounding
-      if (p.dtype) b.chunk = 64;
-      b.M = p.N;
-      b.m_count = r.count;
-      b.N = p.d;
-      b.K = width;
-      b.b_k = v0;
-      b.splits = L.dh_splits;
-      b.acc_in = i > 0 ? slab : nullptr;
-      b.slab_rows = L.rows;
-      if (L.dh_splits > 1 || !last) b.slab = slab;
-      else typed_output(&b, dh, ld_dh, p.dtype, 0);
-      VOCAB_TRY(contract<DH>(G, r.w, nullptr, b, st));
-      if (last && L.dh_splits > 1)
-        VOCAB_TRY((p.dtype ? slab_sum<bf16> : slab_sum<float>)(slab, L.dh_splits, L.rows, p.N, r.count, p.d, r.row_of,
-                                                               dh, ld_dh, 0, st));
+      Args c = b;
+      c.M = p.N;
+      c.m_count = r.count;
+      c.N = p.d;
+      c.K = width;
+      c.b_k = v0;
+      c.max_splits = L.dh_splits;
+      c.acc = L.pieces > 1 ? at<float>(ws, L.acc) : nullptr;
+      c.acc_in = i > 0;
+      c.acc_out = i + 1 < L.pieces;
+      VOCAB_TRY(product<DH>(p, G, r.w, c, dh_slab, dh, ld_dh, 0, st));
     }
     if (dw) {
-      void* out = static_cast<uint8_t*>(dw) + (int64_t)v0 * ld_dw * e;
-      Args b = args_of(p, L, r);
       b.row_of = nullptr;
-      if (p.dtype) b.chunk = 64;
       b.M = width;
       b.N = p.d;
       b.K = p.N;
       b.k_count = r.count;
-      b.splits = L.dw_splits;
-      b.slab_rows = L.piece;
-      if (L.dw_splits > 1) b.slab = at<float>(ws, L.dw);
-      else typed_output(&b, out, ld_dw, p.dtype, accumulate_dw);
-      VOCAB_TRY(contract<DW>(G, r.h, nullptr, b, st));
-      if (L.dw_splits > 1)
-        VOCAB_TRY((p.dtype ? slab_sum<bf16> : slab_sum<float>)(b.slab, L.dw_splits, L.piece, width, nullptr, p.d,
-                                                               nullptr, out, ld_dw, accumulate_dw, st));
+      b.max_splits = L.dw_splits;
+      VOCAB_TRY(product<DW>(p, G, r.h, b, dw_slab, static_cast<uint8_t*>(dw) + (int64_t)v0 * ld_dw * e, ld_dw,
+                            accumulate_dw, st));
     }
   }
   return cudaSuccess;

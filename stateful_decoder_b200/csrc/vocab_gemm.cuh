@@ -8,14 +8,15 @@
 //   STATS  D = h w^T: per row and 128 columns, the maximum and the sum of
 //          exponentials of z = D * inv_t, and z at the row's listed ids
 //   GRAD   D = h w^T: g = c (exp(z - lse) - q), rounded to bf16
-//   GRAD3  the same as three bf16 planes whose sum is g to 2^-24
+//   GRAD2, GRAD3  the same as two or three bf16 planes whose sum is g to
+//          2^-16 or 2^-24
 //   DH     D = g w     (A K-major, B MN-major): fp32 partials or typed rows
 //   DW     D = g^T h   (A and B MN-major): fp32 partials or typed rows
 //
 // fp32 operands are held as three bf16 planes x = x0 + x1 + x2 (24 bits); six
 // products, the smallest first, leave out terms below 2^-24 |x||y|.
 //
-// A CTA has twelve warps: one issues TMA, one MMA, one owns tensor memory,
+// A CTA has twelve warps: two issue TMA, one MMA, one owns tensor memory,
 // eight drain a 128 x 256 accumulator (warps 4-7 its first 128 columns, 8-11
 // the others) while the MMAs fill the second of two.
 //
@@ -37,7 +38,7 @@ constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int kThreads = 384;
 constexpr int kNoId = 0x7fffffff;
 
-enum Kind { STATS, GRAD, GRAD3, DH, DW };
+enum Kind { STATS, GRAD, GRAD2, GRAD3, DH, DW };
 
 // A row's list of (id, probability) as the kernels see it.
 struct RowList {
@@ -56,10 +57,11 @@ struct Args {
   int M, N, K;            // extents; *m_count / *k_count replace M / K where set
   const int32_t* m_count;
   const int32_t* k_count;
-  int terms;              // 1 or 6 plane products
+  int terms;              // 1, 2 or 6 plane products
   int chunk;              // k-blocks per tensor-memory sum (of the leading term)
   int bn;                 // columns per tile, a multiple of 16 up to BN
-  int splits;             // K ranges, one fp32 slab each (DH, DW)
+  int units;              // CTAs or pairs on the device
+  int max_splits;         // K ranges of the last round's tiles at most (DH, DW); see split_rule
   int a_row, a_k, b_row, b_k;  // coordinate offsets of the operands
   // STATS, GRAD
   RowList list;
@@ -72,9 +74,9 @@ struct Args {
   const float* lse;
   const float* weight;
   // DH, DW
-  float* slab;            // fp32 [splits][slab_rows][N]; null: typed output
-  int64_t slab_rows;
-  const float* acc_in;    // added first (same layout as slab), or null
+  float* slab;            // fp32 [splits][last round's tiles][rows of a tile][BN]
+  float* acc;             // fp32 [rows][N]: the sum over pieces of K, or null
+  int acc_in, acc_out;    // add what acc holds; leave the sum there
   void* out;
   int64_t ld_out;
   int out_bf16, accumulate, vec;
@@ -222,7 +224,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Tile {
-  int m, n, kb0, kb1, split;
+  int m, n, kb0, kb1;
+  int split, rest;  // K range and number among the split tiles; split -1: whole
 };
 
 // Stores a 32 x 32 bf16 box (64-byte swizzle) from shared memory; what lies
@@ -235,40 +238,88 @@ __device__ __forceinline__ void store_box(const CUtensorMap* tm, uint32_t src, i
       : "memory");
 }
 
-template <int CG>
-struct Plan {
-  int m_tiles, n_tiles, kb, total_kb, per_split, tiles;
-  __device__ __forceinline__ void init(const Args& a) {
-    const int M = a.m_count ? *a.m_count : a.M, K = a.k_count ? *a.k_count : a.K;
-    m_tiles = (M + BM * CG - 1) / (BM * CG);
-    n_tiles = (a.N + a.bn - 1) / a.bn;
+// K ranges for `tiles` tiles (fewer than a round) on `units` CTAs or pairs:
+// the count that takes the least time, at least 16 k-blocks each and two rounds
+// in all.  A range also writes a slab that is read again, about six k-blocks'
+// time (1.6 us).
+// In whole numbers: host and device have to agree.
+__host__ __device__ inline int split_rule(int tiles, int units, int kblocks, int most) {
+  int best = 1, cost = kblocks;
+  for (int s = 2; s <= most && s * 16 <= kblocks && s * tiles <= 2 * units; ++s) {
+    const int c = (tiles * s + units - 1) / units * ((kblocks + s - 1) / s + 6);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// The tiles of a product.  Whole rounds of the device take whole tiles; the
+// tiles of a last, unfilled round (or of the only one) are split over K.
+struct Cut {
+  int m_tiles, n_tiles, kb, total_kb, whole, rest, splits, per_split, tiles;
+  __device__ __forceinline__ void init(int M, int N, int K, int tile_m, int tile_n, int terms, int units, int most) {
+    m_tiles = (M + tile_m - 1) / tile_m;
+    n_tiles = (N + tile_n - 1) / tile_n;
     kb = (K + BK - 1) / BK;
-    total_kb = kb * a.terms;
-    per_split = (total_kb + a.splits - 1) / a.splits;
-    tiles = m_tiles * n_tiles * a.splits;
+    total_kb = kb * terms;
+    const int all = m_tiles * n_tiles;
+    whole = all;
+    rest = 0;
+    splits = 1;
+    if (most > 1) {
+      const int left = all % units;
+      splits = left ? split_rule(left, units, total_kb, most) : 1;
+      if (splits > 1) {
+        rest = left;
+        whole = all - left;
+      }
+    }
+    per_split = (total_kb + splits - 1) / splits;
+    tiles = whole + rest * splits;
   }
-  // End of the tensor-memory sum that starts at c0.  Of six plane products the
-  // first five add up to 2^-8 of the last, and their error counts as little.
-  __device__ __forceinline__ int chunk_end(const Args& a, int c0, int kb1) const {
-    if (a.terms > 1 && c0 < 5 * kb) return min(kb1, min(c0 + 64, 5 * kb));
-    return min(kb1, c0 + a.chunk);
-  }
-  // Panels of 16 row tiles, columns of tiles inside: the tiles that run
+  // Panels of `gm` row tiles, columns of tiles inside: the tiles that run
   // together share their operands in L2.
-  __device__ __forceinline__ Tile at(int t) const {
-    constexpr int GM = 16 / CG;
-    Tile r;
-    const int mn = m_tiles * n_tiles;
-    r.split = t / mn;
-    t -= r.split * mn;
-    const int p = t / (GM * n_tiles), first = p * GM;
-    const int g = min(m_tiles - first, GM);
+  __device__ __forceinline__ void place(int t, int gm, int* m, int* n) const {
+    const int p = t / (gm * n_tiles), first = p * gm;
+    const int g = min(m_tiles - first, gm);
     const int i = t - first * n_tiles;
-    r.n = i / g;
-    r.m = first + (i - r.n * g);
-    r.kb0 = min(total_kb, r.split * per_split);
-    r.kb1 = min(total_kb, r.kb0 + per_split);
+    *n = i / g;
+    *m = first + (i - *n * g);
+  }
+};
+constexpr int kPanel = 16;  // row tiles of 128 per panel
+
+template <int CG>
+struct Plan : Cut {
+  __device__ __forceinline__ void init(const Args& a) {
+    Cut::init(a.m_count ? *a.m_count : a.M, a.N, a.k_count ? *a.k_count : a.K, BM * CG, a.bn, a.terms, a.units,
+              a.max_splits);
+  }
+  __device__ __forceinline__ Tile at(int t) const {
+    Tile r;
+    r.split = -1;  // whole
+    r.rest = 0;
+    r.kb0 = 0;
+    r.kb1 = total_kb;
+    if (t >= whole) {
+      const int u = t - whole;
+      r.split = u / rest;
+      r.rest = u - r.split * rest;
+      r.kb0 = min(total_kb, r.split * per_split);
+      r.kb1 = min(total_kb, r.kb0 + per_split);
+      t = whole + r.rest;
+    }
+    place(t, kPanel / CG, &r.m, &r.n);
     return r;
+  }
+  // End of the tensor-memory sum that starts at c0.  Of several plane products
+  // all but the last add up to 2^-8 of it, and their error counts as little.
+  __device__ __forceinline__ int chunk_end(const Args& a, int c0, int kb1) const {
+    const int small = (a.terms - 1) * kb;
+    if (c0 < small) return min(kb1, min(c0 + 64, small));
+    return min(kb1, c0 + a.chunk);
   }
 };
 
@@ -385,24 +436,30 @@ __device__ __forceinline__ void store_row32(OT* o, float* v, int left, bool vec,
   }
 }
 
+template <int CG>
 __device__ __forceinline__ void product_epilogue(const Args& a, int64_t i, int64_t n, bool on, int n_tile, int half,
-                                                 int split, float (&x)[4][32]) {
+                                                 float* slab_row, float (&x)[4][32]) {
   if (!on) return;
   const int col0 = n_tile * BN + half * 128;
-  const int64_t slab = ((int64_t)split * a.slab_rows + i) * a.N + col0;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int left = a.N - col0 - c * 32;
     float* v = x[c];
-    if (a.acc_in) {
-      const float* p = a.acc_in + slab + c * 32;
+    if (slab_row) {
+      store_row32(slab_row + half * 128 + c * 32, v, 32, true, false);
+      continue;
+    }
+    if (a.acc) {
+      float* p = a.acc + i * a.N + col0 + c * 32;
+      if (a.acc_out) {
+        store_row32(p, v, left, (a.N & 3) == 0, a.acc_in != 0);
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (j < left) v[j] += p[j];
     }
-    if (a.slab) {
-      store_row32(a.slab + slab + c * 32, v, left, (a.N & 3) == 0, false);
-    } else if (a.out_bf16) {
+    if (a.out_bf16) {
       store_row32(static_cast<bf16*>(a.out) + n * a.ld_out + col0 + c * 32, v, left, a.vec, a.accumulate);
     } else {
       store_row32(static_cast<float*>(a.out) + n * a.ld_out + col0 + c * 32, v, left, a.vec, a.accumulate);
@@ -461,34 +518,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   plan.init(a);
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
-  // Products of planes for fp32 operands, smallest first: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0).
-  if (warp == 0 && lane == 0) {
+  if ((warp == 0 || warp == 3) && lane == 0) {
+    // TMA: warp 0 loads A, warp 3 loads B.  One thread for both was short of
+    // time where an operand takes several boxes (DH, DW: 25 % of the rate).
+    // Products of planes go smallest first: (2,0) (0,2) (1,1) (1,0) (0,1)
+    // (0,0), or (1,0) (0,0); `planes` lists an operand's, last product lowest.
+    const bool is_a = warp == 0;
+    const uint32_t planes = a.terms == 6 ? (is_a ? 0x201100u : 0x021010u) : a.terms == 2 ? (is_a ? 0x10u : 0u) : 0u;
     uint32_t it = 0;
     bool ok = true;
     const uint32_t bytes = C::A_BYTES * CG + (uint32_t)a.bn * BK * 2;
     for (int t = first; t < plan.tiles && ok; t += step) {
       const Tile tile = plan.at(t);
-      const int row_a = tile.m * BM * CG + rank * BM + a.a_row, row_b = tile.n * a.bn + rank * (a.bn / CG) + a.b_row;
+      const int row = is_a ? tile.m * BM * CG + rank * BM + a.a_row : tile.n * a.bn + rank * (a.bn / CG) + a.b_row;
+      const int k_off = is_a ? a.a_k : a.b_k;
+      int turn = tile.kb0 / max(1, plan.kb), kt = tile.kb0 - turn * plan.kb;
       for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {
-        const int term = a.terms == 1 ? 5 : kb / plan.kb;
-        const int k = (a.terms == 1 ? kb : kb - term * plan.kb) * BK;
-        const int plane_a = term == 0 ? 2 : (term == 2 || term == 3) ? 1 : 0;
-        const int plane_b = term == 1 ? 2 : (term == 2 || term == 4) ? 1 : 0;
         const int s = it % S;
         if (!mbar_wait(empty + 8 * s, ((it / S) & 1u) ^ 1u) || *abort_flag) {
           *abort_flag = 1;
           ok = false;
           break;
         }
-        const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
+        const int plane = (planes >> (4 * (a.terms - 1 - turn))) & 15;
+        const uint32_t sa = base + s * C::STAGE;
         uint32_t bar = full + 8 * s;
-        if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
+        if (is_a && rank == 0) mbar_arrive_expect_tx(bar, bytes);
         if constexpr (CG == 2) bar = in_leader(bar);
-        load_tile<CG, BM, A_MN>(sa, &tmA, bar, row_a, k + a.a_k, plane_a);
-        load_tile<CG, C::B_ROWS, B_MN>(sb, &tmB, bar, row_b, k + a.b_k, plane_b);
+        if (is_a) load_tile<CG, BM, A_MN>(sa, &tmA, bar, row, kt * BK + k_off, plane);
+        else load_tile<CG, C::B_ROWS, B_MN>(sa + C::A_BYTES, &tmB, bar, row, kt * BK + k_off, plane);
+        if (++kt == plan.kb) {
+          kt = 0;
+          ++turn;
+        }
       }
     }
-    if (!ok && rank == 0) {  // copies still in flight land before the CTA leaves
+    if (!ok && is_a && rank == 0) {  // copies still in flight land before the CTA leaves
       for (uint32_t i = it > S ? it - S : 0; i < it; ++i) mbar_wait(full + 8 * (i % S), (i / S) & 1u);
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
@@ -540,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t n = on && a.row_of ? a.row_of[i] : i;
       const int v0 = tile.n * a.bn + half * 128 + a.b_row;
       int pos = 0;
-      if constexpr (KIND == STATS || KIND == GRAD || KIND == GRAD3) {
+      if constexpr (KIND != DH && KIND != DW) {
         if (on && a.list.K > 1) pos = lower_bound(a.list.ids + n * a.list.K, a.list.K, v0);
       }
       float x[4][32];
@@ -582,12 +647,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if constexpr (KIND == STATS) stats_epilogue(a, i, n, on, tile.n, half, v0, pos, x);
-      else if constexpr (KIND == GRAD || KIND == GRAD3)
-        grad_epilogue<KIND == GRAD ? 1 : 3>(a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n,
+      else if constexpr (KIND != DH && KIND != DW)
+        grad_epilogue<KIND == GRAD ? 1 : KIND == GRAD2 ? 2 : 3>(a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n,
                                             on, tile.n, half, v0, pos, x);
-      else product_epilogue(a, i, n, on, tile.n, half, tile.split, x);
+      else {
+        float* slab_row = tile.split < 0 ? nullptr
+                                         : a.slab + (((int64_t)tile.split * plan.rest + tile.rest) * (BM * CG) +
+                                                     rank * BM + q * 32 + lane) * BN;
+        product_epilogue<CG>(a, i, n, on, tile.n, half, slab_row, x);
+      }
     }
-    if constexpr (KIND == GRAD || KIND == GRAD3) {
+    if constexpr (KIND == GRAD || KIND == GRAD2 || KIND == GRAD3) {
       if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
