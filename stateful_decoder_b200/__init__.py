@@ -467,29 +467,37 @@ def rlt_op_sample(logits, sampling: dict, t: int, token, logp=None, logmu=None, 
 
 
 # ------------------------------------------------- vocabulary operators
+_DTYPES: dict = {}  # torch dtype -> RLT_DTYPE_*, filled on first use (torch is imported by the calls that need it)
+
+
 def _rows2(t, what: str, rows: int | None = None, cols: int | None = None):
     """(pointer, row distance, dtype) of a CUDA matrix whose rows are
     contiguous and do not overlap; rows may stand apart (a slice of columns)."""
-    n, d = t.shape if t.dim() == 2 else (-1, -1)
+    shape = t.shape
+    n, d = shape if len(shape) == 2 else (-1, -1)
     if n < 0 or (rows is not None and n != rows) or (cols is not None and d != cols):
         raise ValueError(f"{what}: expected shape [{'N' if rows is None else rows}, {'d' if cols is None else cols}], "
-                         f"got {tuple(t.shape)}")
-    dt = _DTYPES.get(str(t.dtype))
+                         f"got {tuple(shape)}")
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32})
+    dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
-    ld = t.stride(0) if n > 1 else max(d, 1)
-    if not t.is_cuda or (d > 1 and t.stride(1) != 1) or ld < d:
+    ld, inner = t.stride()
+    if n <= 1:
+        ld = max(d, 1)
+    if not t.is_cuda or (d > 1 and inner != 1) or ld < d:
         raise ValueError(f"{what}: expected a CUDA matrix with contiguous rows")
     return t.data_ptr(), ld, dt
 
 
-def _vec(t, dtype_name: str, shape: tuple, what: str):
-    if tuple(t.shape) != shape:
+def _vec(t, dtype_name: str, shape: tuple, what: str) -> int:
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    return _dev(t, dtype_name)
-
-
-_DTYPES = {"torch.bfloat16": DTYPE_BF16, "torch.float32": DTYPE_F32}
+    if not t.is_cuda or not t.is_contiguous() or str(t.dtype) != dtype_name:
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor of {dtype_name}")
+    return t.data_ptr()
 
 
 def _same_device(*tensors):
@@ -501,31 +509,32 @@ def _same_device(*tensors):
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{at}")
 
 
-def _with_workspace(call, like, workspace, stream) -> None:
-    """call(ws, size*, stream) with the caller's workspace (a uint8 CUDA
+def _with_workspace(fn, args, like, workspace, stream) -> None:
+    """fn(*args, ws, size*, stream) with the caller's workspace (a uint8 CUDA
     tensor) or one of the size the call asks for, from torch's allocator on
     the stream the call runs on."""
     st = _stream(stream)
+    size = ctypes.c_size_t()
     if workspace is None:
-        need = ctypes.c_size_t()
-        _check(call(None, ctypes.byref(need), st))
+        _check(fn(*args, None, ctypes.byref(size), st))
         import torch
-        n = max(need.value, 256)
+        n = max(size.value, 256)
         if stream is None:
             workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
         else:
             with torch.cuda.stream(torch.cuda.ExternalStream(st.value or 0)):
                 workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
-    ptr = _dev(workspace, "torch.uint8")
-    _check(call(ptr, ctypes.byref(ctypes.c_size_t(workspace.numel())), st))
+    size.value = workspace.numel()
+    _check(fn(*args, _vec(workspace, "torch.uint8", workspace.shape, "workspace"), ctypes.byref(size), st))
 
 
 def _vocab(h, w):
     hp, ld_h, dt = _rows2(h, "h")
-    wp, ld_w, wt = _rows2(w, "w", cols=h.shape[1])
+    N, d = h.shape
+    wp, ld_w, wt = _rows2(w, "w", cols=d)
     if wt != dt:
         raise ValueError(f"h is {h.dtype}, w is {w.dtype}")
-    return Vocab(h=hp, ld_h=ld_h, w=wp, ld_w=ld_w, N=h.shape[0], V=w.shape[0], d=h.shape[1], dtype=dt)
+    return Vocab(hp, ld_h, wp, ld_w, N, w.shape[0], d, dt)
 
 
 def _vocab_grads(h, w, dh, dw):
@@ -550,7 +559,7 @@ def rlt_op_cross_entropy(h, w, target, logp, lse, workspace=None, stream=None) -
     _same_device(h, w, target, logp, lse, workspace)
     args = (ctypes.byref(a), _vec(target, "torch.int32", (N,), "target"), _vec(logp, "torch.float32", (N,), "logp"),
             _vec(lse, "torch.float32", (N,), "lse"))
-    _with_workspace(lambda ws, n, st: _lib.rlt_op_cross_entropy(*args, ws, n, st), h, workspace, stream)
+    _with_workspace(_lib.rlt_op_cross_entropy, args, h, workspace, stream)
 
 
 def rlt_op_cross_entropy_backward(h, w, target, lse, weight, dh=None, dw=None, accumulate: bool = False,
@@ -562,7 +571,7 @@ def rlt_op_cross_entropy_backward(h, w, target, lse, weight, dh=None, dw=None, a
     _same_device(h, w, target, lse, weight, dh, dw, workspace)
     args = (ctypes.byref(a), _vec(target, "torch.int32", (N,), "target"), _vec(lse, "torch.float32", (N,), "lse"),
             _vec(weight, "torch.float32", (N,), "weight"), *_vocab_grads(h, w, dh, dw), int(accumulate))
-    _with_workspace(lambda ws, n, st: _lib.rlt_op_cross_entropy_backward(*args, ws, n, st), h, workspace, stream)
+    _with_workspace(_lib.rlt_op_cross_entropy_backward, args, h, workspace, stream)
 
 
 def _teacher(N, ids, teacher):
@@ -581,7 +590,7 @@ def rlt_op_distill(h, w, ids, teacher, temperature: float, kl, lse, workspace=No
     _same_device(h, w, ids, teacher, kl, lse, workspace)
     args = (ctypes.byref(a), *_teacher(N, ids, teacher), temperature, _vec(kl, "torch.float32", (N,), "kl"),
             _vec(lse, "torch.float32", (N,), "lse"))
-    _with_workspace(lambda ws, n, st: _lib.rlt_op_distill(*args, ws, n, st), h, workspace, stream)
+    _with_workspace(_lib.rlt_op_distill, args, h, workspace, stream)
 
 
 def rlt_op_distill_backward(h, w, ids, teacher, temperature: float, lse, weight, dh=None, dw=None,
@@ -592,7 +601,7 @@ def rlt_op_distill_backward(h, w, ids, teacher, temperature: float, lse, weight,
     _same_device(h, w, ids, teacher, lse, weight, dh, dw, workspace)
     args = (ctypes.byref(a), *_teacher(N, ids, teacher), temperature, _vec(lse, "torch.float32", (N,), "lse"),
             _vec(weight, "torch.float32", (N,), "weight"), *_vocab_grads(h, w, dh, dw), int(accumulate))
-    _with_workspace(lambda ws, n, st: _lib.rlt_op_distill_backward(*args, ws, n, st), h, workspace, stream)
+    _with_workspace(_lib.rlt_op_distill_backward, args, h, workspace, stream)
 
 
 def rlt_op_embed(emb, tokens, out, scale: float = 1.0, stream=None) -> None:
@@ -616,7 +625,7 @@ def rlt_op_embed_backward(dout, tokens, demb, scale: float = 1.0, accumulate: bo
     ep, ld_e, et = _rows2(demb, "demb")
     _same_device(dout, tokens, demb, workspace)
     args = (gp, ld_g, gt, _vec(tokens, "torch.int32", (N,), "tokens"), N, V, d, scale, ep, ld_e, et, int(accumulate))
-    _with_workspace(lambda ws, n, st: _lib.rlt_op_embed_backward(*args, ws, n, st), demb, workspace, stream)
+    _with_workspace(_lib.rlt_op_embed_backward, args, demb, workspace, stream)
 
 
 def rlt_check_device() -> None:

@@ -153,11 +153,28 @@ struct Gather {
   int planes;
 };
 
+// Does row n take part?  Both loads are issued whatever the first says.
+__device__ __forceinline__ bool row_on(const Gather& g, int64_t n) {
+  const float w = g.weight ? g.weight[n] : 1.f;
+  return takes_part(g.list, n, g.V) & (w != 0.f);
+}
+// How many of the rows before `end` take part (every thread gets it).
 __device__ __forceinline__ int count_rows(const Gather& g, int64_t end, int* red) {
   int n_on = 0;
-#pragma unroll 8
-  for (int64_t n = threadIdx.x; n < end; n += 256)
-    n_on += takes_part(g.list, n, g.V) && (g.weight == nullptr || g.weight[n] != 0.f);
+  for (int64_t n0 = threadIdx.x; n0 < end; n0 += 256 * 8) {
+    float w[8], some[8];
+    int32_t id[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t n = n0 + u * 256;
+      const bool in = n < end;
+      w[u] = !in ? 0.f : g.weight ? g.weight[n] : 1.f;
+      some[u] = in && g.list.some ? g.list.some[n] : 0.f;
+      id[u] = in && !g.list.some ? g.list.ids[n] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) n_on += (w[u] != 0.f) & ((some[u] != 0.f) | (id[u] >= 0 && id[u] < g.V));
+  }
   n_on = __reduce_add_sync(0xffffffffu, n_on);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n_on;
   __syncthreads();
@@ -181,7 +198,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const Gather g) {
     int at = count_rows(g, min((int64_t)g.N, n0), red);
     for (int64_t r = n0; r < min((int64_t)g.N, n0 + g.rows_per_block); r += 8) {
       const int64_t n = r + warp;
-      const bool on = n < g.N && takes_part(g.list, n, g.V) && (g.weight == nullptr || g.weight[n] != 0.f);
+      const bool on = n < g.N && row_on(g, n);
       if (lane == 0) red[warp] = on;
       __syncthreads();
       int before = 0, all = 0;
@@ -353,18 +370,17 @@ __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
 
 // ------------------------------------------------------------------ few rows
 // Statistics of up to 8 rows: bound by reading w once, so w goes through
-// registers and h through shared memory, in fp32.  A warp takes R rows of w at
-// a time (16-byte loads, 256 columns per step) against all NB rows of h; the
-// R x NB sums of its lanes are added by exchanging halves, after which lane
-// r * NB + n holds z of w row r and h row n.
-// At V = 32000, d = 2048, one row: see the table of DESIGN for its time
-// against the tensor-core path, which reads w at 4.1 TB/s here (every SM asks
-// for the same 128 bytes of h at a time).
-template <typename T, int NB>
-struct FewCfg {
-  static constexpr int R = NB == 8 ? 4 : 8;
-  static constexpr int WARPS = 16;
-};
+// registers (16-byte loads, the next step's in flight under this one's
+// products) and h through shared memory, in fp32.  A warp takes two to four
+// rows of w at a time against all NB rows of h; the sums of its lanes are added by
+// exchanging halves, after which lane r * NB + n holds z of w row r and h row n.
+// At V = 32000, d = 2048, one row: 28 us, where the tensor-core path takes 42:
+// there every SM asks L2 for the same 128 bytes of h at a time.
+// Rows of w per group: few, so that the groups spread evenly over the warps
+// (at V = 32000 four per group leave a round 38 % full), but four where each
+// read of h from shared memory has to serve more products.
+template <int NB>
+constexpr int kFewW = NB <= 2 ? 2 : 4;
 constexpr int kFewRows = 8;
 constexpr size_t kFewSmem = 200 << 10;  // h in shared memory
 
@@ -394,14 +410,36 @@ struct Raw<float> {
 
 template <typename T, int NB>
 __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld_h, const T* w, int64_t ld_w, int N,
-                                                          int V, int d, int vec, float scale, RowList list,
+                                                          int V, int d, int vec, float scale, RowList list, int early,
                                                           float2* part, int64_t part_ld, float* zsel) {
-  constexpr int R = FewCfg<T, NB>::R;
+  constexpr int R = kFewW<NB>;
+  constexpr int U = (sizeof(T) == 2 ? 8 : 4) / R;  // groups of 256 columns per step
   extern __shared__ float4 hs[];  // [NB][2][d8]: the two halves of every group of eight
   __shared__ float2 sums[16][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d8 = (d + 7) / 8;
-  griddep_enter();
+  const int steps = (d8 + 32 * U - 1) / (32 * U);
+  const int groups = (V + R - 1) / R, stride = (int)gridDim.x * 16;
+  const int g0 = warp * (int)gridDim.x + (int)blockIdx.x;
+  const int total = g0 < groups ? ((groups - 1 - g0) / stride + 1) * steps : 0;
+  if (!early) griddep_enter();
+  Raw<T> cur[U][R], nxt[U][R];
+  int f_step = 0, f_v = g0 * R;  // what is fetched next
+  auto fetch = [&](Raw<T>(&x)[U][R]) {
+    const int c = f_step * (32 * U) + lane;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const T* row = w + (int64_t)min(f_v + i, V - 1) * ld_w;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if ((c + u * 32) * 8 + 8 <= d) x[u][i].load(row + (c + u * 32) * 8);
+    }
+    if (++f_step == steps) {
+      f_step = 0;
+      f_v += stride * R;
+    }
+  };
+  if (vec && total > 0) fetch(cur);
   for (int i = threadIdx.x; i < NB * d8 * 2; i += 512) {
     const int n = i / (d8 * 2), r = i - n * d8 * 2, half = r / d8, g = r - half * d8;
     float v[4];
@@ -412,36 +450,40 @@ __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld
     }
     hs[i] = make_float4(v[0], v[1], v[2], v[3]);
   }
+  if (early) griddep_enter();
   __syncthreads();
   const int n = lane % NB, r = lane / NB;  // what this lane finishes
   const bool mine = lane < R * NB && n < N;
   int pos = 0, next = mine ? list.ids[(int64_t)n * list.K] : kNoId;
   float m = -INFINITY, s = 0.f;
-  const int groups = (V + R - 1) / R, step = (int)gridDim.x * 16;
-  for (int g = warp * (int)gridDim.x + (int)blockIdx.x; g < groups; g += step) {
-    float acc[R * NB];
+  float acc[R * NB];
 #pragma unroll
-    for (int i = 0; i < R * NB; ++i) acc[i] = 0.f;
-    const int64_t v0 = (int64_t)g * R;
-    for (int c = lane; c < d8; c += 32) {
-      Raw<T> x[R];
+  for (int i = 0; i < R * NB; ++i) acc[i] = 0.f;
+  int step = 0;
+  int64_t v0 = (int64_t)g0 * R;
+#pragma unroll 2
+  for (int it = 0; it < total; ++it) {
+    if (vec && it + 1 < total) fetch(nxt);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = step * (32 * U) + u * 32 + lane;
+      if (c >= d8) continue;
       if (vec && c * 8 + 8 <= d) {
-#pragma unroll
-        for (int i = 0; i < R; ++i) x[i].load(w + min(v0 + i, (int64_t)V - 1) * ld_w + c * 8);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const float4 lo = hs[(b * 2) * d8 + c], hi = hs[(b * 2 + 1) * d8 + c];
 #pragma unroll
           for (int i = 0; i < R; ++i) {
+            const Raw<T>& x = cur[u][i];
             float& t = acc[i * NB + b];
-            t = fmaf(x[i].get(0), lo.x, t);
-            t = fmaf(x[i].get(1), lo.y, t);
-            t = fmaf(x[i].get(2), lo.z, t);
-            t = fmaf(x[i].get(3), lo.w, t);
-            t = fmaf(x[i].get(4), hi.x, t);
-            t = fmaf(x[i].get(5), hi.y, t);
-            t = fmaf(x[i].get(6), hi.z, t);
-            t = fmaf(x[i].get(7), hi.w, t);
+            t = fmaf(x.get(0), lo.x, t);
+            t = fmaf(x.get(1), lo.y, t);
+            t = fmaf(x.get(2), lo.z, t);
+            t = fmaf(x.get(3), lo.w, t);
+            t = fmaf(x.get(4), hi.x, t);
+            t = fmaf(x.get(5), hi.y, t);
+            t = fmaf(x.get(6), hi.z, t);
+            t = fmaf(x.get(7), hi.w, t);
           }
         }
       } else {
@@ -457,7 +499,14 @@ __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld
         }
       }
     }
-    // sums over the lanes: value i ends in lane i (values beyond 32 lanes' worth of halvings stay whole)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < R; ++i) cur[u][i] = nxt[u][i];
+    if (++step != steps) continue;
+    step = 0;
+    // the group's sums over the lanes: value i ends in lane i
+    __syncwarp();
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) {
       if (off >= R * NB) {
@@ -486,6 +535,10 @@ __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld
       s = (s == 0.f ? 0.f : s * expf(m - ref)) + expf(z - ref);
       m = mn;
     }
+    __syncwarp();
+    v0 += (int64_t)stride * R;
+#pragma unroll
+    for (int i = 0; i < R * NB; ++i) acc[i] = 0.f;
   }
   sums[warp][lane] = make_float2(m, s);
   __syncthreads();
@@ -786,7 +839,8 @@ cudaError_t few_rows(const VocabLoss& p, const Layout& L, const RowList& list, f
   VOCAB_TRY((set_smem<few_rows_kernel<T, NB>>((int)kFewSmem)));
   const int vec = vector_rows(p.w, p.ld_w, p.dtype);
   return launch_pdl(few_rows_kernel<T, NB>, dim3((unsigned)L.parts), dim3(512), smem, st, static_cast<const T*>(p.h),
-                    p.ld_h, static_cast<const T*>(p.w), p.ld_w, p.N, p.V, p.d, vec, p.inv_t, list, part,
+                    p.ld_h, static_cast<const T*>(p.w), p.ld_w, p.N, p.V, p.d, vec, p.inv_t, list,
+                    (int)(p.teacher != nullptr), part,
                     (int64_t)kFewRows, zsel);
 }
 template <typename T>
@@ -842,6 +896,9 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
     a.N = p.V;
     a.K = p.d;
     a.bn = L.bn;
+    // The list kernel before this one let it start after its own wait, so h
+    // and w are complete: only the epilogue waits for the lists.
+    a.early = p.teacher != nullptr && !L.gather && !L.pack_w;
     a.part = part;
     a.part_ld = L.rows;
     a.zsel = zsel;

@@ -64,6 +64,7 @@ struct Args {
   int max_splits;         // K ranges of the last round's tiles at most (DH, DW); see split_rule
   int a_row, a_k, b_row, b_k;  // coordinate offsets of the operands
   // STATS, GRAD
+  int early;              // operands are older than the kernel before this one: loads do not wait for it
   RowList list;
   const int32_t* row_of;  // compact row -> row, or null
   int V;
@@ -508,9 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
   }
-  griddep_enter();
+  if (!a.early) griddep_enter();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (a.early && warp >= 4) griddep_enter();
   if constexpr (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
