@@ -104,14 +104,30 @@ __device__ __forceinline__ void planes8(bf16* dst, int64_t plane, int planes, fl
     for (int j = 0; j < 8; ++j) v[j] -= to_f32(from_f32<bf16>(v[j]));
   }
 }
-// One row by a warp, four groups of eight in flight per lane.
+// One row by a warp, several groups of eight in flight per lane.
 template <typename T>
 __device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out, int64_t plane, int planes) {
   const int lane = threadIdx.x & 31;
-  for (int c0 = lane * 8; c0 < d; c0 += 1024) {
-    float v[4][8];
+  if constexpr (sizeof(T) == 2) {
+    if (vec) {  // one plane: the bits as they are
+      const int d8 = d / 8;
+      for (int c0 = lane; c0 < d8; c0 += 128) {
+        uint4 v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 4; ++u)
+          if (c0 + u * 32 < d8) v[u] = reinterpret_cast<const uint4*>(x)[c0 + u * 32];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c0 + u * 32 < d8) reinterpret_cast<uint4*>(out)[c0 + u * 32] = v[u];
+      }
+      for (int c = d8 * 8 + lane; c < d; c += 32) out[c] = x[c];
+      return;
+    }
+  }
+  for (int c0 = lane * 8; c0 < d; c0 += 512) {
+    float v[2][8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
       const int c = c0 + u * 256;
       if (vec && c + 8 <= d) {
         load8(x + c, v[u]);
@@ -121,7 +137,7 @@ __device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out,
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 2; ++u)
       if (c0 + u * 256 < d) planes8(out + c0 + u * 256, plane, planes, v[u]);
   }
 }
@@ -142,6 +158,7 @@ struct Gather {
   float *loss, *lse;    // forward: zeros for the others
   void* dh;             // backward: a zero row for the others
   int64_t ld_dh;
+  int vec_dh;
   // rows of w to `w_out`
   int w_blocks;
   const void* w;
@@ -188,7 +205,7 @@ __device__ __forceinline__ int count_rows(const Gather& g, int64_t end, int* red
 // (each counts the rows before its own), blocks that zero the rows behind the
 // last one up to a multiple of 128, blocks that convert w.
 template <typename T>
-__global__ void __launch_bounds__(256) gather_kernel(const Gather g) {
+__global__ void __launch_bounds__(256, 4) gather_kernel(const Gather g) {
   griddep_enter();
   __shared__ int red[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -217,8 +234,14 @@ __global__ void __launch_bounds__(256) gather_kernel(const Gather g) {
           g.loss[n] = 0.f;
           g.lse[n] = 0.f;
         }
-        if (g.dh)
-          for (int c = lane; c < g.d; c += 32) static_cast<T*>(g.dh)[n * g.ld_dh + c] = from_f32<T>(0.f);
+        if (g.dh) {
+          T* o = static_cast<T*>(g.dh) + n * g.ld_dh;
+          const float z[8] = {};
+          if (g.vec_dh && g.d % 8 == 0)
+            for (int c = lane * 8; c < g.d; c += 256) store8(o + c, z);
+          else
+            for (int c = lane; c < g.d; c += 32) o[c] = from_f32<T>(0.f);
+        }
       }
     }
     return;
@@ -786,8 +809,9 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
   if (L.gather) {
     g.list = r->list;
     g.weight = weight;
-    // At most 1024 blocks, each of which counts all rows before its own.
-    g.rows_per_block = (int)round_up((p.N + 1023) / 1024, 8);
+    // One wave of blocks, each of which counts all rows before its own.
+    constexpr int kWave = 4 * kSmCount;
+    g.rows_per_block = (int)round_up((p.N + kWave - 1) / kWave, 8);
     g.row_blocks = (p.N + g.rows_per_block - 1) / g.rows_per_block;
     g.pad_blocks = 16;
     g.h = p.h;
@@ -801,6 +825,7 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
     g.lse = lse;
     g.dh = dh;
     g.ld_dh = ld_dh;
+    g.vec_dh = dh && vector_rows(dh, ld_dh, p.dtype);
     r->row_of = g.row_of;
     r->count = g.count;
     r->h = Matrix{g.h_out, L.rows, p.d, L.ld, g.h_plane, L.planes};
