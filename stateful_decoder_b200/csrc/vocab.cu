@@ -12,6 +12,7 @@
 // are left out before the contractions: the rows that remain are gathered, in
 // order, into one bf16 operand, and every extent follows their count on the
 // device.
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include <algorithm>
@@ -104,6 +105,16 @@ __device__ __forceinline__ void planes8(bf16* dst, int64_t plane, int planes, fl
     for (int j = 0; j < 8; ++j) v[j] -= to_f32(from_f32<bf16>(v[j]));
   }
 }
+// 8 elements from column c of a row (zeros past d).
+template <typename T>
+__device__ __forceinline__ void row8(const T* row, int c, int d, bool vec, float* v) {
+  if (vec && c + 8 <= d) {
+    load8(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < d ? to_f32(row[c + j]) : 0.f;
+  }
+}
 // One row by a warp, several groups of eight in flight per lane.
 template <typename T>
 __device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out, int64_t plane, int planes) {
@@ -127,19 +138,54 @@ __device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out,
   for (int c0 = lane * 8; c0 < d; c0 += 512) {
     float v[2][8];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = c0 + u * 256;
-      if (vec && c + 8 <= d) {
-        load8(x + c, v[u]);
-      } else if (c < d) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[u][j] = c + j < d ? to_f32(x[c + j]) : 0.f;
-      }
-    }
+    for (int u = 0; u < 2; ++u) row8(x, c0 + u * 256, d, vec, v[u]);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
       if (c0 + u * 256 < d) planes8(out + c0 + u * 256, plane, planes, v[u]);
   }
+}
+// One row as two fp16 planes of x * 2^e; returns 2^-e.
+__device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __half* out, int64_t plane) {
+  const int lane = threadIdx.x & 31;
+  float m = 0.f;
+  for (int c0 = lane * 8; c0 < d; c0 += 512) {
+    float v[2][8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) row8(x, c0 + u * 256, d, vec, v[u]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(v[0][j]), fabsf(v[1][j])));
+  }
+  m = warp_max(m);
+  // exponent of the largest element; 2^e within the normal numbers
+  const int top = (int)(__float_as_uint(m) >> 23) - 127;
+  const int e = max(-112, min(126, 14 - top));
+  const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+  for (int c0 = lane * 8; c0 < d; c0 += 512) {
+    float v[2][8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) row8(x, c0 + u * 256, d, vec, v[u]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (c0 + u * 256 >= d) continue;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        __half2 h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float &a = v[u][2 * j], &b = v[u][2 * j + 1];
+          if (p == 0) {
+            a *= up;
+            b *= up;
+          }
+          h[j] = __floats2half2_rn(a, b);
+          a -= __low2float(h[j]);
+          b -= __high2float(h[j]);
+        }
+        *reinterpret_cast<uint4*>(out + p * plane + c0 + u * 256) = *reinterpret_cast<const uint4*>(h);
+      }
+    }
+  }
+  return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
 struct Gather {
@@ -167,8 +213,23 @@ struct Gather {
   bf16* w_out;
   int64_t w_plane;
   int64_t ld_out;
-  int planes;
+  int planes;           // bf16 planes (0: none wanted)
+  // fp32: the fp16 planes and their rows' 2^-e, or null
+  __half *h16, *w16;
+  float *h_inv, *w_inv;
 };
+// A row of h or w in all the forms wanted.
+template <typename T>
+__device__ __forceinline__ void convert_row(const T* x, int d, bool vec, bf16* out, int64_t plane, int planes,
+                                            __half* out16, float* inv) {
+  if (planes) copy_row(x, d, vec, out, plane, planes);
+  if constexpr (sizeof(T) == 4) {
+    if (out16) {
+      const float i = fp16_row(x, d, vec, out16, plane);
+      if ((threadIdx.x & 31) == 0) *inv = i;
+    }
+  }
+}
 
 // Does row n take part?  Both loads are issued whatever the first says.
 __device__ __forceinline__ bool row_on(const Gather& g, int64_t n) {
@@ -228,7 +289,8 @@ __global__ void __launch_bounds__(256, 4) gather_kernel(const Gather g) {
       at += all;
       if (on) {
         if (lane == 0) g.row_of[i] = (int32_t)n;
-        copy_row(static_cast<const T*>(g.h) + n * g.ld_h, g.d, g.vec_h, g.h_out + i * g.ld_out, g.h_plane, g.planes);
+        convert_row(static_cast<const T*>(g.h) + n * g.ld_h, g.d, g.vec_h, g.h_out + i * g.ld_out, g.h_plane, g.planes,
+                    g.h16 ? g.h16 + i * g.ld_out : nullptr, g.h_inv + i);
       } else if (n < g.N) {
         if (g.loss && lane == 0) {
           g.loss[n] = 0.f;
@@ -261,7 +323,8 @@ __global__ void __launch_bounds__(256, 4) gather_kernel(const Gather g) {
   b -= g.pad_blocks;
   const int64_t v = (int64_t)b * 8 + warp;
   if (v < g.V)
-    copy_row(static_cast<const T*>(g.w) + v * g.ld_w, g.d, g.vec_w, g.w_out + v * g.ld_out, g.w_plane, g.planes);
+    convert_row(static_cast<const T*>(g.w) + v * g.ld_w, g.d, g.vec_w, g.w_out + v * g.ld_out, g.w_plane, g.planes,
+                g.w16 ? g.w16 + v * g.ld_out : nullptr, g.w_inv + v);
 }
 
 // Joins the statistics of a row's column groups, in a fixed order, and writes
@@ -595,7 +658,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// A bf16 operand in memory: `planes` matrices [rows][cols], rows ld apart.
+// A 16-bit operand in memory: `planes` matrices [rows][cols], rows ld apart.
 struct Matrix {
   const bf16* p;
   int64_t rows, cols, ld, plane;
@@ -675,9 +738,10 @@ cudaError_t contract(const Matrix& A, const Matrix& B, const Matrix* G, const Ar
 
 // Where things lie in the workspace, and how the work is cut.
 struct Layout {
-  size_t sid = 0, sq = 0, slogq = 0, some = 0, row_of = 0, count = 0, h = 0, w = 0, part = 0, zsel = 0, g = 0,
+  size_t sid = 0, sq = 0, slogq = 0, some = 0, row_of = 0, count = 0, h = 0, w = 0, h16 = 0, w16 = 0, h_inv = 0,
+         w_inv = 0, part = 0, zsel = 0, g = 0,
          dh = 0, dw = 0, acc = 0, total = 0;
-  int planes = 1, terms = 1;      // of h and w, and of h w^T
+  int planes = 1, terms = 1;      // bf16 planes of h and w; products of h w^T
   int g_planes = 1, g_terms = 1;  // of g, and of its products
   bool few = false, gather = true, pack_w = false;
   int64_t rows = 0;  // rows of the gathered operand, a multiple of 256
@@ -712,8 +776,8 @@ Layout layout(const VocabLoss& p, int backward) {
     return at;
   };
   const bool f32 = p.dtype == 0;
-  L.planes = f32 ? 3 : 1;
-  L.terms = f32 ? 6 : 1;
+  L.planes = !f32 ? 1 : backward ? 3 : 0;
+  L.terms = f32 ? 3 : 1;
   L.rows = round_up(std::max(p.N, 1), 256);
   L.ld = round_up(p.d, 8);
   const size_t n = (size_t)p.N;
@@ -734,6 +798,12 @@ Layout layout(const VocabLoss& p, int backward) {
     L.h = take((size_t)L.planes * L.rows * L.ld * 2);
   }
   if (L.pack_w) L.w = take((size_t)L.planes * p.V * L.ld * 2);
+  if (f32 && !L.few) {
+    L.h16 = take((size_t)2 * L.rows * L.ld * 2);
+    L.w16 = take((size_t)2 * p.V * L.ld * 2);
+    L.h_inv = take((size_t)L.rows * 4);
+    L.w_inv = take((size_t)(round_up(p.V, BN) + BN) * 4);  // tiles read past V
+  }
   const int64_t n_tiles = (p.V + BN - 1) / BN;
   if (!backward) {
     L.parts = (int)(2 * n_tiles);
@@ -779,7 +849,9 @@ struct Prepared {
   RowList list;
   const float* slogq = nullptr;
   const int32_t *row_of = nullptr, *count = nullptr;
-  Matrix h, w;
+  const float *h_inv = nullptr, *w_inv = nullptr;
+  Matrix h, w;    // of the products of g
+  Matrix zh, zw;  // of the logits
 };
 
 int vector_rows(const void* p, int64_t ld, int dtype) {
@@ -799,6 +871,8 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
   }
   r->h = Matrix{static_cast<const bf16*>(p.h), p.N, p.d, p.ld_h, 0, 1};
   r->w = Matrix{static_cast<const bf16*>(p.w), p.V, p.d, p.ld_w, 0, 1};
+  r->zh = r->h;
+  r->zw = r->w;
   if (!L.gather && !L.pack_w) return cudaSuccess;
   Gather g{};
   g.N = p.N;
@@ -828,7 +902,7 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
     g.vec_dh = dh && vector_rows(dh, ld_dh, p.dtype);
     r->row_of = g.row_of;
     r->count = g.count;
-    r->h = Matrix{g.h_out, L.rows, p.d, L.ld, g.h_plane, L.planes};
+    r->zh = r->h = Matrix{g.h_out, L.rows, p.d, L.ld, g.h_plane, L.planes};
   }
   if (L.pack_w) {
     g.w_blocks = (p.V + 7) / 8;
@@ -837,7 +911,15 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
     g.vec_w = vector_rows(p.w, p.ld_w, p.dtype);
     g.w_out = at<bf16>(ws, L.w);
     g.w_plane = (int64_t)p.V * L.ld;
-    r->w = Matrix{g.w_out, p.V, p.d, L.ld, g.w_plane, L.planes};
+    r->zw = r->w = Matrix{g.w_out, p.V, p.d, L.ld, g.w_plane, L.planes};
+  }
+  if (p.dtype == 0) {
+    g.h16 = at<__half>(ws, L.h16);
+    g.w16 = at<__half>(ws, L.w16);
+    r->h_inv = g.h_inv = at<float>(ws, L.h_inv);
+    r->w_inv = g.w_inv = at<float>(ws, L.w_inv);
+    r->zh = Matrix{reinterpret_cast<const bf16*>(g.h16), L.rows, p.d, L.ld, g.h_plane, 2};
+    r->zw = Matrix{reinterpret_cast<const bf16*>(g.w16), p.V, p.d, L.ld, g.w_plane, 2};
   }
   const dim3 grid((unsigned)(g.row_blocks + g.pad_blocks + g.w_blocks));
   return p.dtype ? launch_pdl(gather_kernel<bf16>, grid, dim3(256), 0, st, g)
@@ -847,6 +929,9 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
 Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
   Args a{};
   a.terms = L.terms;
+  a.fp16 = p.dtype == 0;
+  a.h_inv = r.h_inv;
+  a.w_inv = r.w_inv;
   a.chunk = p.dtype ? 16 : 4;
   a.bn = BN;
   a.max_splits = 1;
@@ -927,7 +1012,7 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
     a.part = part;
     a.part_ld = L.rows;
     a.zsel = zsel;
-    VOCAB_TRY(contract<STATS>(r.h, r.w, nullptr, a, st));
+    VOCAB_TRY(contract<STATS>(r.zh, r.zw, nullptr, a, st));
   }
   return launch_pdl(join_kernel, dim3((unsigned)((p.N + 31) / 32)), dim3(1024), 0, st, (const float2*)part, L.parts,
                     L.few ? (int64_t)kFewRows : L.rows, p.N, r.row_of, r.count, p.V, r.list, r.slogq,
@@ -956,11 +1041,12 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.b_row = v0;
     a.lse = lse;
     a.weight = weight;
-    VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(r.h, r.w, &G, a, st)
-              : L.g_planes == 2 ? contract<GRAD2>(r.h, r.w, &G, a, st)
-                                : contract<GRAD3>(r.h, r.w, &G, a, st));
+    VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(r.zh, r.zw, &G, a, st)
+              : L.g_planes == 2 ? contract<GRAD2>(r.zh, r.zw, &G, a, st)
+                                : contract<GRAD3>(r.zh, r.zw, &G, a, st));
     Args b = args_of(p, L, r);
     b.terms = L.g_terms;
+    b.fp16 = 0;
     if (dh) {
       Args c = b;
       c.M = p.N;

@@ -13,8 +13,13 @@
 //   DH     D = g w     (A K-major, B MN-major): fp32 partials or typed rows
 //   DW     D = g^T h   (A and B MN-major): fp32 partials or typed rows
 //
-// fp32 operands are held as three bf16 planes x = x0 + x1 + x2 (24 bits); six
-// products, the smallest first, leave out terms below 2^-24 |x||y|.
+// fp32 operands are held as 16-bit planes whose products add up.  For the
+// logits: two fp16 planes of x * 2^e, e per row so that the row's largest
+// element is near 2^15 (11 + 11 bits and a sign: x to 2^-24 of itself, or
+// 2^-39 of the row's largest); three products, and the powers of two are taken
+// back in the epilogue.  For the products of g, whose columns differ by more
+// than fp16 can hold: three bf16 planes x = x0 + x1 + x2 (24 bits), six
+// products; what is left out is below 2^-24 |x||y|.  Smallest products first.
 //
 // A CTA has twelve warps: two issue TMA, one MMA, one owns tensor memory,
 // eight drain a 128 x 256 accumulator (warps 4-7 its first 128 columns, 8-11
@@ -57,7 +62,8 @@ struct Args {
   int M, N, K;            // extents; *m_count / *k_count replace M / K where set
   const int32_t* m_count;
   const int32_t* k_count;
-  int terms;              // 1, 2 or 6 plane products
+  int terms;              // 1, 2, 3 or 6 plane products
+  int fp16;               // the operands' type: bf16 or fp16
   int chunk;              // k-blocks per tensor-memory sum (of the leading term)
   int bn;                 // columns per tile, a multiple of 16 up to BN
   int units;              // CTAs or pairs on the device
@@ -66,6 +72,7 @@ struct Args {
   // STATS, GRAD
   int early;              // operands are older than the kernel before this one: loads do not wait for it
   RowList list;
+  const float *h_inv, *w_inv;  // fp16 planes: 2^-e of the rows of h and w, or null
   const int32_t* row_of;  // compact row -> row, or null
   int V;
   float scale;            // inv_t
@@ -327,6 +334,22 @@ struct Plan : Cut {
 // ---------------------------------------------------------------- epilogues
 // Each handles the 128 columns from n_tile * BN + half * 128 of one row per
 // thread, in registers.
+// Takes the operands' powers of two back; columns past the matrix are ignored
+// by what follows.
+__device__ __forceinline__ void unscale(const Args& a, int64_t i, bool on, int v0, float (&x)[4][32]) {
+  const float hi = on ? a.h_inv[i] : 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 w = *reinterpret_cast<const float4*>(a.w_inv + v0 + c * 32 + j);
+      x[c][j] *= hi * w.x;
+      x[c][j + 1] *= hi * w.y;
+      x[c][j + 2] *= hi * w.z;
+      x[c][j + 3] *= hi * w.w;
+    }
+}
+
 __device__ __forceinline__ void stats_epilogue(const Args& a, int64_t i, int64_t n, bool on, int n_tile, int half,
                                                int v0, int pos, float (&x)[4][32]) {
   const float s2 = a.scale * kLog2e;
@@ -524,9 +547,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // TMA: warp 0 loads A, warp 3 loads B.  One thread for both was short of
     // time where an operand takes several boxes (DH, DW: 25 % of the rate).
     // Products of planes go smallest first: (2,0) (0,2) (1,1) (1,0) (0,1)
-    // (0,0), or (1,0) (0,0); `planes` lists an operand's, last product lowest.
+    // (0,0), or the last three, or (1,0) (0,0); `planes` lists an operand's,
+    // last product lowest.
     const bool is_a = warp == 0;
-    const uint32_t planes = a.terms == 6 ? (is_a ? 0x201100u : 0x021010u) : a.terms == 2 ? (is_a ? 0x10u : 0u) : 0u;
+    const uint32_t planes = a.terms == 6   ? (is_a ? 0x201100u : 0x021010u)
+                            : a.terms == 3 ? (is_a ? 0x100u : 0x010u)
+                            : a.terms == 2 ? (is_a ? 0x10u : 0u)
+                                           : 0u;
     uint32_t it = 0;
     bool ok = true;
     const uint32_t bytes = C::A_BYTES * CG + (uint32_t)a.bn * BK * 2;
@@ -559,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t i = it > S ? it - S : 0; i < it; ++i) mbar_wait(full + 8 * (i % S), (i / S) & 1u);
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
-    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
+    const uint32_t idesc = (1u << 4) | (a.fp16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
                            ((uint32_t)(a.bn >> 3) << 17) | ((uint32_t)(BM * CG >> 4) << 24);
     uint32_t it = 0, n_acc = 0;
     bool ok = true;
@@ -648,6 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      if constexpr (KIND == STATS || KIND == GRAD3) {
+        if (a.h_inv) unscale(a, i, on, v0, x);
+      }
       if constexpr (KIND == STATS) stats_epilogue(a, i, n, on, tile.n, half, v0, pos, x);
       else if constexpr (KIND != DH && KIND != DW)
         grad_epilogue<KIND == GRAD ? 1 : KIND == GRAD2 ? 2 : 3>(a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n,
