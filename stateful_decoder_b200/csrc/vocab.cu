@@ -393,10 +393,10 @@ __global__ void __launch_bounds__(1024) join_kernel(const float2* part, int part
 
 // out rows of the tiles whose K was split = the slabs' sum in order.
 struct SlabSum {
-  const float* slab;
+  const float4* slab;
   int M, N, K;
   const int32_t *m_count, *k_count;
-  int terms, units, max_splits, cg;
+  int terms, units, max_splits, cg, bn;
   const int32_t* row_of;
   void* out;
   int64_t ld;
@@ -410,22 +410,32 @@ __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
   const int M = a.m_count ? *a.m_count : a.M, K = a.k_count ? *a.k_count : a.K;
   const int tile_rows = BM * a.cg;
   Cut cut;
-  cut.init(M, a.N, K, tile_rows, BN, a.terms, a.units, a.max_splits);
-  const int total = cut.rest * tile_rows * (BN / 8);
-  const int64_t stride = (int64_t)cut.rest * tile_rows * BN;
+  cut.init(M, a.N, K, tile_rows, a.bn, a.terms, a.units, a.max_splits);
+  const int total = cut.rest * tile_rows * (BN / 8), tile = tile_rows * (BN / 4);
+  const int64_t stride = (int64_t)cut.rest * tile;
   for (int e = (int)blockIdx.x * 256 + threadIdx.x; e < total; e += (int)gridDim.x * 256) {
-    const int c = e % (BN / 8) * 8, row = e / (BN / 8);
+    const int row = e % tile_rows, c = e / tile_rows % (BN / 8) * 8, rest = e / (tile_rows * (BN / 8));
     int m, nt;
-    cut.place(cut.whole + row / tile_rows, kPanel / a.cg, &m, &nt);
-    const int64_t i = (int64_t)m * tile_rows + row % tile_rows;
-    const int col = nt * BN + c;
-    if (i >= M || col >= a.N) continue;
+    cut.place(cut.whole + rest, kPanel / a.cg, &m, &nt);
+    const int64_t i = (int64_t)m * tile_rows + row;
+    const int col = nt * a.bn + c;
+    if (i >= M || c >= a.bn || col >= a.N) continue;
+    const float4* p = a.slab + (int64_t)rest * tile + c / 4 * tile_rows + row;
     float s[8] = {};
-    for (int k = 0; k < cut.splits; ++k) {
-      float v[8];
-      load8(a.slab + k * stride + (int64_t)row * BN + c, v);
+    for (int k0 = 0; k0 < cut.splits; k0 += 4) {
+      float4 lo[4], hi[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += v[j];
+      for (int u = 0; u < 4; ++u)
+        if (k0 + u < cut.splits) {
+          lo[u] = p[(k0 + u) * stride];
+          hi[u] = p[(k0 + u) * stride + tile_rows];
+        }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k0 + u < cut.splits) {
+          s[0] += lo[u].x; s[1] += lo[u].y; s[2] += lo[u].z; s[3] += lo[u].w;
+          s[4] += hi[u].x; s[5] += hi[u].y; s[6] += hi[u].z; s[7] += hi[u].w;
+        }
     }
     if (a.acc) {
       float* p = a.acc + i * a.N + col;
@@ -699,11 +709,14 @@ cudaError_t set_smem(int bytes) {
 }
 
 template <int KIND, int CG>
-cudaError_t launch(const Matrix& A, const Matrix& B, const Matrix* G, const Args& a, cudaStream_t st) {
+cudaError_t launch(const Matrix& A, const Matrix& B, const Matrix* G, Args a, cudaStream_t st) {
   using C = Cfg<CG>;
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
   CUtensorMap ta, tb, tg;
-  VOCAB_TRY(tensor_map(&ta, A, A_MN ? 64 : BM));
+  a.stages = std::min(C::MOST_STAGES, C::PIPE / (C::A_BYTES + a.bn / CG * BK * 2));
+  // (a box of rows that are not there costs as much as one of rows that are)
+  a.a_rows = A_MN ? BM : (int)std::min<int64_t>(BM, round_up(a.M, 8));
+  VOCAB_TRY(tensor_map(&ta, A, A_MN ? 64 : a.a_rows));
   VOCAB_TRY(tensor_map(&tb, B, B_MN ? 64 : a.bn / CG));
   if (G) VOCAB_TRY(tensor_map(&tg, *G, 32, 32));
   else tg = ta;
@@ -752,20 +765,54 @@ struct Layout {
 
 bool tma_ready(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
 
-constexpr int kMostSplits = 16;
+constexpr int kMostSplits = 64;
 int cta_group(int M) { return M > BM ? 2 : 1; }
 // Floats that the split sums of a product can take: split_rule makes at most
 // two rounds of split tiles, and none of fewer than 32 k-blocks.
 int64_t slab_floats(int64_t M, int64_t N, int64_t kblocks, int* most) {
   *most = kblocks >= 32 ? kMostSplits : 1;
   if (*most == 1) return 0;
-  const int64_t n_tiles = (N + BN - 1) / BN;
+  const int64_t n_tiles = (N + 63) / 64;  // of the narrowest
   int64_t need = 0;
   for (int cg = 1; cg <= 2; ++cg) {
     const int64_t all = (M + BM * cg - 1) / (BM * cg) * n_tiles;
     need = std::max(need, std::min<int64_t>(2 * (kSmCount / cg), all * kMostSplits) * BM * cg * BN);
   }
   return need;
+}
+
+// Columns per tile of the logits: the width whose rounds take the least time,
+// a tile costing its columns and some more for its rows' operand (128 where
+// the tensor cores are the limit: 192 columns ran at 0.87 of the rate of 256;
+// 64 where reading w is).  Narrow tiles where one round would leave SMs idle.
+// (The gradient writes 64 columns at a time.)
+int logit_columns(int64_t M, int64_t V, int backward) {
+  const int cg = cta_group((int)M);
+  const int64_t units = kSmCount / cg, m_tiles = (M + BM * cg - 1) / (BM * cg);
+  int best = BN;
+  int64_t cost = INT64_MAX;
+  for (int bn = BN; bn >= 64; bn -= backward || cg == 2 ? 64 : 32) {
+    const int64_t c = (m_tiles * ((V + bn - 1) / bn) + units - 1) / units * (bn + (m_tiles > 1 ? 128 : 64));
+    if (c < cost) {
+      cost = c;
+      best = bn;
+    }
+  }
+  return best;
+}
+// Columns per tile of a product with d columns (its idle SMs take ranges of K).
+int product_columns(int64_t M, int64_t d) {
+  const int step = 64 * cta_group((int)M);
+  int best = BN;
+  int64_t cost = INT64_MAX;
+  for (int bn = BN; bn >= step; bn -= step) {
+    const int64_t c = (d + bn - 1) / bn * (bn + 64);
+    if (c < cost) {
+      cost = c;
+      best = bn;
+    }
+  }
+  return best;
 }
 
 Layout layout(const VocabLoss& p, int backward) {
@@ -805,17 +852,9 @@ Layout layout(const VocabLoss& p, int backward) {
     L.w_inv = take((size_t)(round_up(p.V, BN) + BN) * 4);  // tiles read past V
   }
   const int64_t n_tiles = (p.V + BN - 1) / BN;
+  L.bn = logit_columns(p.N, p.V, backward);
   if (!backward) {
-    L.parts = (int)(2 * n_tiles);
-    if (L.few) {
-      L.parts = (int)std::min<int64_t>(kSmCount, (p.V + 15) / 16);
-    } else if (p.N <= BM) {
-      // One row tile: the work is reading w once.  Columns per tile so that
-      // the tiles fill whole rounds of the SMs evenly.
-      const int64_t rounds = (n_tiles + kSmCount - 1) / kSmCount;
-      L.bn = std::max(32, (int)round_up((p.V + kSmCount * rounds - 1) / (kSmCount * rounds), 16));
-      L.parts = 2 * ((p.V + L.bn - 1) / L.bn);
-    }
+    L.parts = L.few ? (int)std::min<int64_t>(kSmCount, (p.V + 15) / 16) : 2 * ((p.V + L.bn - 1) / L.bn);
     L.part = take((size_t)L.parts * (L.few ? kFewRows : L.rows) * 8);
     L.zsel = take(n * p.K * 4);
     return L;
@@ -964,10 +1003,11 @@ cudaError_t few_rows_of(const VocabLoss& p, const Layout& L, const RowList& list
 
 // A product of g into typed rows, K split where the rule says so.
 template <int KIND>
-cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a, float* slab, void* out, int64_t ld,
+cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a, float4* slab, void* out, int64_t ld,
                     int accumulate, cudaStream_t st) {
   const int cg = cta_group(a.M);
   a.units = kSmCount / cg;
+  a.bn = product_columns(a.M, a.N);
   a.slab = slab;
   a.out = out;
   a.ld_out = ld;
@@ -979,7 +1019,7 @@ cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a
   VOCAB_TRY(contract<KIND>(G, B, nullptr, a, st));
   if (a.max_splits == 1) return cudaSuccess;
   const SlabSum s{slab,    a.M,          a.N, a.K,      a.m_count, a.k_count, a.terms,
-                  a.units, a.max_splits, cg,  a.row_of, out,       ld,        accumulate, a.vec,
+                  a.units, a.max_splits, cg, a.bn, a.row_of, out,       ld,        accumulate, a.vec,
                   a.acc,   a.acc_in,     a.acc_out};
   const dim3 grid((unsigned)std::min<int64_t>(4 * kSmCount, ((int64_t)a.M * a.N + 2047) / 2048));
   return p.dtype ? launch_pdl(slab_sum_kernel<bf16>, grid, dim3(256), 0, st, s)
@@ -1029,7 +1069,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
   const Layout L = layout(p, 1);
   Prepared r;
   VOCAB_TRY(prepare(p, L, ws, weight, nullptr, nullptr, dh, ld_dh, &r, st));
-  float *dh_slab = at<float>(ws, L.dh), *dw_slab = at<float>(ws, L.dw);
+  float4 *dh_slab = at<float4>(ws, L.dh), *dw_slab = at<float4>(ws, L.dw);
   const Matrix G{at<bf16>(ws, L.g), L.rows, L.piece, L.piece, L.rows * L.piece, L.g_planes};
   for (int i = 0; i < L.pieces; ++i) {
     const int v0 = i * L.piece, width = std::min(p.V - v0, L.piece);
@@ -1041,6 +1081,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.b_row = v0;
     a.lse = lse;
     a.weight = weight;
+    a.bn = L.bn;
     VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(r.zh, r.zw, &G, a, st)
               : L.g_planes == 2 ? contract<GRAD2>(r.zh, r.zw, &G, a, st)
                                 : contract<GRAD3>(r.zh, r.zw, &G, a, st));

@@ -65,7 +65,9 @@ struct Args {
   int terms;              // 1, 2, 3 or 6 plane products
   int fp16;               // the operands' type: bf16 or fp16
   int chunk;              // k-blocks per tensor-memory sum (of the leading term)
-  int bn;                 // columns per tile, a multiple of 16 up to BN
+  int bn;                 // columns per tile: a multiple of 32 (GRAD: 64; DH, DW: 64 per CTA) up to BN
+  int stages;             // of bn's size
+  int a_rows;             // rows of A that a tile loads (fewer than BM when M is: the rest are never looked at)
   int units;              // CTAs or pairs on the device
   int max_splits;         // K ranges of the last round's tiles at most (DH, DW); see split_rule
   int a_row, a_k, b_row, b_k;  // coordinate offsets of the operands
@@ -82,7 +84,7 @@ struct Args {
   const float* lse;
   const float* weight;
   // DH, DW
-  float* slab;            // fp32 [splits][last round's tiles][rows of a tile][BN]
+  float4* slab;           // [splits][last round's tiles][BN / 4][rows of a tile]: a warp's rows side by side
   float* acc;             // fp32 [rows][N]: the sum over pieces of K, or null
   int acc_in, acc_out;    // add what acc holds; leave the sum there
   void* out;
@@ -93,11 +95,9 @@ struct Args {
 template <int CG>
 struct Cfg {
   static constexpr int A_BYTES = BM * BK * 2;
-  static constexpr int B_ROWS = BN / CG;
-  static constexpr int B_BYTES = B_ROWS * BK * 2;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = CG == 1 ? 4 : 6;
-  static constexpr int OUT_OFF = STAGES * STAGE;    // 8 warps x two 32 x 32 bf16 boxes
+  static constexpr int PIPE = 196608;               // 4 or 6 stages of the largest tile, up to 12 of smaller ones
+  static constexpr int MOST_STAGES = 12;
+  static constexpr int OUT_OFF = PIPE;              // 8 warps x two 32 x 32 bf16 boxes
   static constexpr int BAR_OFF = OUT_OFF + 8 * 4096;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
 };
@@ -130,13 +130,13 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* tm, ui
         : "memory");
 }
 
-// One operand tile of ROWS rows (or columns) and 64 of k: K-major as ROWS
-// rows of 128 bytes, MN-major as ROWS / 64 boxes of 64 k-rows.
-template <int CG, int ROWS, bool MN>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int row, int k, int plane) {
+// One operand tile of `rows` rows (or columns) and 64 of k: K-major as rows of
+// 128 bytes, MN-major as rows / 64 boxes of 64 k-rows.
+template <int CG, bool MN>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int rows, int row, int k,
+                                          int plane) {
   if constexpr (MN) {
-#pragma unroll
-    for (int i = 0; i < ROWS / 64; ++i) load_box<CG>(dst + i * 8192, tm, bar, row + 64 * i, k, plane);
+    for (int i = 0; i < rows / 64; ++i) load_box<CG>(dst + i * 8192, tm, bar, row + 64 * i, k, plane);
   } else {
     load_box<CG>(dst, tm, bar, k, row, plane);
   }
@@ -246,15 +246,18 @@ __device__ __forceinline__ void store_box(const CUtensorMap* tm, uint32_t src, i
       : "memory");
 }
 
-// K ranges for `tiles` tiles (fewer than a round) on `units` CTAs or pairs:
-// the count that takes the least time, at least 16 k-blocks each and two rounds
-// in all.  A range also writes a slab that is read again, about six k-blocks'
-// time (1.6 us).
+// K ranges for `tiles` tiles (fewer than a round) on `units` CTAs or pairs, at
+// least 16 k-blocks each: as many as fill one round, or two, whichever takes
+// less time.  A range also writes a slab that is read again, about 12
+// k-blocks' time (3 us), and the sum is a launch of its own.
 // In whole numbers: host and device have to agree.
 __host__ __device__ inline int split_rule(int tiles, int units, int kblocks, int most) {
   int best = 1, cost = kblocks;
-  for (int s = 2; s <= most && s * 16 <= kblocks && s * tiles <= 2 * units; ++s) {
-    const int c = (tiles * s + units - 1) / units * ((kblocks + s - 1) / s + 6);
+  const int limit = kblocks / 16 < most ? kblocks / 16 : most;
+  for (int rounds = 1; rounds <= 2; ++rounds) {
+    const int fill = rounds * units / tiles, s = fill < limit ? fill : limit;
+    if (s < 2) continue;
+    const int c = (tiles * s + units - 1) / units * ((kblocks + s - 1) / s + 12) + 12;
     if (c < cost) {
       cost = c;
       best = s;
@@ -388,8 +391,10 @@ __device__ __forceinline__ void grad_epilogue(const Args& a, const CUtensorMap* 
                                               int lane, int64_t n, bool on, int n_tile, int half, int v0, int pos,
                                               float (&x)[4][32]) {
   const float s2 = a.scale * kLog2e;
-  const int col0 = n_tile * BN + half * 128;
-  const int cols = min(128, a.N - col0);
+  const int col0 = n_tile * a.bn + half * 128;
+  const int cols = min(min(128, a.bn - half * 128), a.N - col0);
+  // what is written: whole k-blocks of the products to come, zeros past N
+  const int out_cols = min(min(128, a.bn - half * 128), (a.N + BK - 1) / BK * BK - col0);
   const float cw = on ? a.weight[n] * a.scale : 0.f;
   const float sub = on ? a.lse[n] * kLog2e : 0.f;
   int next = on && pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
@@ -400,7 +405,7 @@ __device__ __forceinline__ void grad_epilogue(const Args& a, const CUtensorMap* 
     if (on) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = cw * ex2(fmaf(v[j], s2, -sub));
-      while (next >= v0 + c * 32 && next < v0 + c * 32 + 32) {
+      while (next >= v0 + c * 32 && next < v0 + min(c * 32 + 32, cols)) {
         sub_at(v, next - v0 - c * 32, cw * (a.list.q ? a.list.q[n * a.list.K + pos] : 1.f));
         next = ++pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
       }
@@ -414,6 +419,7 @@ __device__ __forceinline__ void grad_epilogue(const Args& a, const CUtensorMap* 
     }
 #pragma unroll
     for (int p = 0; p < PLANES; ++p) {
+      if (c * 32 >= out_cols) continue;  // an even number of chunks is written: the buffers keep alternating
       const uint32_t buf = stage + (uint32_t)((c * PLANES + p) & 1) * 2048;
       if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       __syncwarp();
@@ -462,15 +468,19 @@ __device__ __forceinline__ void store_row32(OT* o, float* v, int left, bool vec,
 
 template <int CG>
 __device__ __forceinline__ void product_epilogue(const Args& a, int64_t i, int64_t n, bool on, int n_tile, int half,
-                                                 float* slab_row, float (&x)[4][32]) {
+                                                 float4* slab_row, float (&x)[4][32]) {
   if (!on) return;
-  const int col0 = n_tile * BN + half * 128;
+  const int col0 = n_tile * a.bn + half * 128;
+  const int cols = min(a.bn - half * 128, a.N - col0);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int left = a.N - col0 - c * 32;
+    const int left = cols - c * 32;
+    if (left <= 0) return;
     float* v = x[c];
     if (slab_row) {
-      store_row32(slab_row + half * 128 + c * 32, v, 32, true, false);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        slab_row[(half * 32 + c * 8 + j / 4) * (BM * CG)] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
       continue;
     }
     if (a.acc) {
@@ -498,13 +508,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmG, const Args a) {
   using C = Cfg<CG>;
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
-  constexpr int S = C::STAGES;
+  const int S = a.stages;
+  const uint32_t stage_bytes = C::A_BYTES + (uint32_t)a.bn / CG * (BK * 2);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_u32(smem);
   const uint32_t bars = base + C::BAR_OFF;
-  const uint32_t full = bars, empty = bars + 8 * S, acc_full = bars + 16 * S, acc_empty = acc_full + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 16 * S + 32);
+  constexpr int MS = C::MOST_STAGES;
+  const uint32_t full = bars, empty = bars + 8 * MS, acc_full = bars + 16 * MS, acc_empty = acc_full + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 16 * MS + 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cta_rank();
@@ -554,28 +566,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                             : a.terms == 3 ? (is_a ? 0x100u : 0x010u)
                             : a.terms == 2 ? (is_a ? 0x10u : 0u)
                                            : 0u;
-    uint32_t it = 0;
+    int slot = 0, issued = 0;
+    uint32_t phase = 0;
     bool ok = true;
-    const uint32_t bytes = C::A_BYTES * CG + (uint32_t)a.bn * BK * 2;
+    const uint32_t bytes = (uint32_t)(a.a_rows * CG + a.bn) * (BK * 2);
     for (int t = first; t < plan.tiles && ok; t += step) {
       const Tile tile = plan.at(t);
       const int row = is_a ? tile.m * BM * CG + rank * BM + a.a_row : tile.n * a.bn + rank * (a.bn / CG) + a.b_row;
       const int k_off = is_a ? a.a_k : a.b_k;
       int turn = tile.kb0 / max(1, plan.kb), kt = tile.kb0 - turn * plan.kb;
-      for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {
-        const int s = it % S;
-        if (!mbar_wait(empty + 8 * s, ((it / S) & 1u) ^ 1u) || *abort_flag) {
+      for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
+        if (!mbar_wait(empty + 8 * slot, phase ^ 1u) || *abort_flag) {
           *abort_flag = 1;
           ok = false;
           break;
         }
         const int plane = (planes >> (4 * (a.terms - 1 - turn))) & 15;
-        const uint32_t sa = base + s * C::STAGE;
-        uint32_t bar = full + 8 * s;
+        const uint32_t sa = base + slot * stage_bytes;
+        uint32_t bar = full + 8 * slot;
         if (is_a && rank == 0) mbar_arrive_expect_tx(bar, bytes);
         if constexpr (CG == 2) bar = in_leader(bar);
-        if (is_a) load_tile<CG, BM, A_MN>(sa, &tmA, bar, row, kt * BK + k_off, plane);
-        else load_tile<CG, C::B_ROWS, B_MN>(sa + C::A_BYTES, &tmB, bar, row, kt * BK + k_off, plane);
+        if (is_a) load_tile<CG, A_MN>(sa, &tmA, bar, BM, row, kt * BK + k_off, plane);
+        else load_tile<CG, B_MN>(sa + C::A_BYTES, &tmB, bar, a.bn / CG, row, kt * BK + k_off, plane);
+        issued = min(S, issued + 1);
+        if (++slot == S) {
+          slot = 0;
+          phase ^= 1u;
+        }
         if (++kt == plan.kb) {
           kt = 0;
           ++turn;
@@ -583,12 +600,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && is_a && rank == 0) {  // copies still in flight land before the CTA leaves
-      for (uint32_t i = it > S ? it - S : 0; i < it; ++i) mbar_wait(full + 8 * (i % S), (i / S) & 1u);
+      for (int i = issued; i > 0; --i) {  // the last `issued` slots, oldest first
+        const int at = slot - i;
+        mbar_wait(full + 8 * (at < 0 ? at + S : at), at < 0 ? phase ^ 1u : phase);
+      }
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     const uint32_t idesc = (1u << 4) | (a.fp16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
                            ((uint32_t)(a.bn >> 3) << 17) | ((uint32_t)(BM * CG >> 4) << 24);
-    uint32_t it = 0, n_acc = 0;
+    int slot = 0;
+    uint32_t phase = 0, n_acc = 0;
     bool ok = true;
     for (int t = first; t < plan.tiles && ok; t += step) {
       const Tile tile = plan.at(t);
@@ -602,22 +623,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + as * BN;
-        for (int kb = c0; kb < c1; ++kb, ++it) {
-          const int s = it % S;
-          if (!mbar_wait(full + 8 * s, (it / S) & 1u) || *abort_flag) {
+        for (int kb = c0; kb < c1; ++kb) {
+          if (!mbar_wait(full + 8 * slot, phase) || *abort_flag) {
             *abort_flag = 1;
             ok = false;
             break;
           }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t sa = base + s * C::STAGE, sb = sa + C::A_BYTES;
+          const uint32_t sa = base + slot * stage_bytes, sb = sa + C::A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t da = A_MN ? sdesc(sa + kk * 2048, 8192) : sdesc(sa + kk * 32, 16);
             const uint64_t db = B_MN ? sdesc(sb + kk * 2048, 8192) : sdesc(sb + kk * 32, 16);
             mma<CG>(d, da, db, idesc, kb > c0 || kk > 0);
           }
-          commit<CG>(empty + 8 * s);
+          commit<CG>(empty + 8 * slot);
+          if (++slot == S) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
         if (ok) commit<CG>(acc_full + 8 * as);
       }
@@ -683,9 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         grad_epilogue<KIND == GRAD ? 1 : KIND == GRAD2 ? 2 : 3>(a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n,
                                             on, tile.n, half, v0, pos, x);
       else {
-        float* slab_row = tile.split < 0 ? nullptr
-                                         : a.slab + (((int64_t)tile.split * plan.rest + tile.rest) * (BM * CG) +
-                                                     rank * BM + q * 32 + lane) * BN;
+        float4* slab_row = tile.split < 0 ? nullptr
+                                          : a.slab + ((int64_t)tile.split * plan.rest + tile.rest) * (BM * CG * BN / 4) +
+                                                rank * BM + q * 32 + lane;
         product_epilogue<CG>(a, i, n, on, tile.n, half, slab_row, x);
       }
     }
