@@ -175,6 +175,14 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
@@ -517,8 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int MS = C::MOST_STAGES;
   const uint32_t full = bars, empty = bars + 8 * MS, acc_full = bars + 16 * MS, acc_empty = acc_full + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 16 * MS + 32);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cta_rank();
 
   if (threadIdx.x == 0) {
@@ -530,7 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(acc_full + 8 * s, 1);
       mbar_init(acc_empty + 8 * s, 8 * CG);
     }
-    *abort_flag = 0;
     fence_mbar_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
@@ -555,9 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   plan.init(a);
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
-  if ((warp == 0 || warp == 3) && lane == 0) {
-    // TMA: warp 0 loads A, warp 3 loads B.  One thread for both was short of
-    // time where an operand takes several boxes (DH, DW: 25 % of the rate).
+  // The loops below run in whole warps with one elected lane at work: what
+  // they count is then uniform and stays in uniform registers, where TMA and
+  // MMA take their operands from.  (In a branch of lane 0 alone, moving them
+  // there held the MMA warp to 640 cycles per k-block, whatever its width.)
+  // A wait that runs out ends its role; the others' waits then run out too.
+  if (warp == 0 || warp == 3) {
+    // TMA: warp 0 loads A, warp 3 loads B.
     // Products of planes go smallest first: (2,0) (0,2) (1,1) (1,0) (0,1)
     // (0,0), or the last three, or (1,0) (0,0); `planes` lists an operand's,
     // last product lowest.
@@ -570,24 +580,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     const uint32_t bytes = (uint32_t)(a.a_rows * CG + a.bn) * (BK * 2);
+    const int k_off = is_a ? a.a_k : a.b_k;
     for (int t = first; t < plan.tiles && ok; t += step) {
       const Tile tile = plan.at(t);
       const int row = is_a ? tile.m * BM * CG + rank * BM + a.a_row : tile.n * a.bn + rank * (a.bn / CG) + a.b_row;
-      const int k_off = is_a ? a.a_k : a.b_k;
       int turn = tile.kb0 / max(1, plan.kb), kt = tile.kb0 - turn * plan.kb;
       for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
-        if (!mbar_wait(empty + 8 * slot, phase ^ 1u) || *abort_flag) {
-          *abort_flag = 1;
+        if (!mbar_wait(empty + 8 * slot, phase ^ 1u)) {
           ok = false;
           break;
         }
+        __syncwarp();
         const int plane = (planes >> (4 * (a.terms - 1 - turn))) & 15;
         const uint32_t sa = base + slot * stage_bytes;
         uint32_t bar = full + 8 * slot;
-        if (is_a && rank == 0) mbar_arrive_expect_tx(bar, bytes);
-        if constexpr (CG == 2) bar = in_leader(bar);
-        if (is_a) load_tile<CG, A_MN>(sa, &tmA, bar, BM, row, kt * BK + k_off, plane);
-        else load_tile<CG, B_MN>(sa + C::A_BYTES, &tmB, bar, a.bn / CG, row, kt * BK + k_off, plane);
+        if (elect_one()) {
+          if (is_a && rank == 0) mbar_arrive_expect_tx(bar, bytes);
+          if constexpr (CG == 2) bar = in_leader(bar);
+          if (is_a) load_tile<CG, A_MN>(sa, &tmA, bar, BM, row, kt * BK + k_off, plane);
+          else load_tile<CG, B_MN>(sa + C::A_BYTES, &tmB, bar, a.bn / CG, row, kt * BK + k_off, plane);
+        }
+        __syncwarp();
         issued = min(S, issued + 1);
         if (++slot == S) {
           slot = 0;
@@ -605,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(full + 8 * (at < 0 ? at + S : at), at < 0 ? phase ^ 1u : phase);
       }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     const uint32_t idesc = (1u << 4) | (a.fp16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
                            ((uint32_t)(a.bn >> 3) << 17) | ((uint32_t)(BM * CG >> 4) << 24);
     int slot = 0;
@@ -616,34 +629,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c0 = tile.kb0, c1; c0 < tile.kb1 && ok; c0 = c1, ++n_acc) {
         c1 = plan.chunk_end(a, c0, tile.kb1);
         const uint32_t as = n_acc & 1u;
-        if (!mbar_wait(acc_empty + 8 * as, ((n_acc >> 1) & 1u) ^ 1u) || *abort_flag) {
-          *abort_flag = 1;
+        if (!mbar_wait(acc_empty + 8 * as, ((n_acc >> 1) & 1u) ^ 1u)) {
           ok = false;
           break;
         }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + as * BN;
         for (int kb = c0; kb < c1; ++kb) {
-          if (!mbar_wait(full + 8 * slot, phase) || *abort_flag) {
-            *abort_flag = 1;
+          if (!mbar_wait(full + 8 * slot, phase)) {
             ok = false;
             break;
           }
+          __syncwarp();
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t sa = base + slot * stage_bytes, sb = sa + C::A_BYTES;
+          const uint64_t da = A_MN ? sdesc(sa, 8192) : sdesc(sa, 16), db = B_MN ? sdesc(sb, 8192) : sdesc(sb, 16);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t da = A_MN ? sdesc(sa + kk * 2048, 8192) : sdesc(sa + kk * 32, 16);
-            const uint64_t db = B_MN ? sdesc(sb + kk * 2048, 8192) : sdesc(sb + kk * 32, 16);
-            mma<CG>(d, da, db, idesc, kb > c0 || kk > 0);
+            for (int kk = 0; kk < BK / 16; ++kk)  // the address field counts 16 bytes
+              mma<CG>(d, da + kk * (A_MN ? 128 : 2), db + kk * (B_MN ? 128 : 2), idesc, kb > c0 || kk > 0);
+            commit<CG>(empty + 8 * slot);
+            if (kb + 1 == c1) commit<CG>(acc_full + 8 * as);
           }
-          commit<CG>(empty + 8 * slot);
+          __syncwarp();
           if (++slot == S) {
             slot = 0;
             phase ^= 1u;
           }
         }
-        if (ok) commit<CG>(acc_full + 8 * as);
       }
     }
   } else if (warp >= 4) {
@@ -671,8 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int c0 = tile.kb0; c0 < tile.kb1; c0 = plan.chunk_end(a, c0, tile.kb1), ++n_acc) {
         const uint32_t as = n_acc & 1u;
-        if (!mbar_wait(acc_full + 8 * as, (n_acc >> 1) & 1u) || *abort_flag) {
-          *abort_flag = 1;
+        if (!mbar_wait(acc_full + 8 * as, (n_acc >> 1) & 1u)) {
           ok = false;
           break;
         }
