@@ -158,11 +158,22 @@ struct ZeroRows {
 __device__ __forceinline__ void zero_rows(const ZeroRows& z, int b, int blocks, int threads) {
   const int64_t unit = z.vec ? 16 : z.elem;
   const int64_t per_row = z.row_bytes / unit;
-  const bool whole = z.row_bytes == z.ld_bytes;
-  const int64_t n = per_row * z.V, step = (int64_t)blocks * threads;
-  const int64_t end = n * (z.part + 1) / z.parts;
-  for (int64_t i = n * z.part / z.parts + (int64_t)b * threads + threadIdx.x; i < end; i += step) {
-    uint8_t* p = z.p + (whole ? i * unit : i / per_row * z.ld_bytes + i % per_row * unit);
+  const int64_t n = per_row * z.V, step = (int64_t)blocks * threads, end = n * (z.part + 1) / z.parts;
+  int64_t i = n * z.part / z.parts + (int64_t)b * threads + threadIdx.x;
+  if (z.vec && z.row_bytes == z.ld_bytes) {
+    uint4* p = reinterpret_cast<uint4*>(z.p);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (; i + 3 * step < end; i += 4 * step) {
+      p[i] = zero;
+      p[i + step] = zero;
+      p[i + 2 * step] = zero;
+      p[i + 3 * step] = zero;
+    }
+    for (; i < end; i += step) p[i] = zero;
+    return;
+  }
+  for (; i < end; i += step) {
+    uint8_t* p = z.p + i / per_row * z.ld_bytes + i % per_row * unit;
     if (z.vec) *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
     else if (z.elem == 4) *reinterpret_cast<uint32_t*>(p) = 0;
     else *reinterpret_cast<uint16_t*>(p) = 0;

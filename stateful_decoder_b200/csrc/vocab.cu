@@ -26,73 +26,88 @@ namespace {
 
 using namespace vocab_tc;
 
-constexpr int kMaxK = 256;
-
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
 // ------------------------------------------------------------------ teacher lists
 // One warp per row: q = softmax(teacher * inv_t) over the valid slots, the
-// slots sorted by id (and slot, so the order never depends on timing); empty
-// slots go last.  some[n] = 0 when no slot carries weight.
+// slots sorted by id (and slot, so the order never depends on timing) in a
+// bitonic network over P >= K keys in shared memory, P / 2 exchanges per stage
+// spread over all lanes; empty slots go last.  some[n] = 0 when no slot
+// carries weight.
+template <int P>
 __global__ void __launch_bounds__(128) teacher_prep_kernel(const int32_t* ids, const float* teacher, int N, int K,
                                                            int V, float inv_t, int32_t* sid, float* sq, float* slogq,
                                                            float* some) {
   griddep_enter();
-  __shared__ unsigned long long keys[4][kMaxK];
+  __shared__ unsigned long long keys_s[4][P];
+  __shared__ float t_s[4][P];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t n = (int64_t)blockIdx.x * 4 + warp;
   if (n >= N) return;
-  int P = 32;
-  while (P < K) P <<= 1;
+  unsigned long long* keys = keys_s[warp];
+  float* ts = t_s[warp];
   float m = -INFINITY;
   bool nan = false;
+#pragma unroll
   for (int k = lane; k < P; k += 32) {
     const int32_t id = k < K ? ids[n * K + k] : -1;
+    const float t = k < K ? teacher[n * K + k] * inv_t : 0.f;
     const bool ok = id >= 0 && id < V;
     if (ok) {
-      const float t = teacher[n * K + k] * inv_t;
       nan |= isnan(t);
       m = fmaxf(m, t);
     }
-    keys[warp][k] = ((unsigned long long)(ok ? id : kNoId) << 32) | (unsigned)k;
+    keys[k] = ((unsigned long long)(ok ? id : kNoId) << 32) | (unsigned)k;
+    ts[k] = t;
   }
   m = warp_max(m);
-  const bool any_nan = __any_sync(0xffffffffu, nan);
-  const bool has = m > -INFINITY || any_nan;
+  const bool has = m > -INFINITY || __any_sync(0xffffffffu, nan);
   __syncwarp();
+#pragma unroll 1
   for (int size = 2; size <= P; size <<= 1)
+#pragma unroll 1
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      for (int i = lane; i < P; i += 32) {
-        const int j = i ^ stride;
-        if (j > i) {
-          const unsigned long long a = keys[warp][i], b = keys[warp][j];
-          const bool up = (i & size) == 0;
-          if ((a > b) == up) {
-            keys[warp][i] = b;
-            keys[warp][j] = a;
-          }
+#pragma unroll
+      for (int p = lane; p < P / 2; p += 32) {
+        const int i = ((p & ~(stride - 1)) << 1) | (p & (stride - 1)), j = i + stride;
+        const unsigned long long a = keys[i], b = keys[j];
+        if ((a > b) == ((i & size) == 0)) {
+          keys[i] = b;
+          keys[j] = a;
         }
       }
       __syncwarp();
     }
   float sum = 0.f;
-  for (int k = lane; k < K; k += 32) {
-    const unsigned long long key = keys[warp][k];
-    if ((int)(key >> 32) != kNoId) sum += expf(teacher[n * K + (unsigned)key] * inv_t - m);
+#pragma unroll
+  for (int k = lane; k < P; k += 32) {
+    const unsigned long long key = keys[k];
+    if ((int)(key >> 32) != kNoId) sum += expf(ts[(unsigned)key] - m);
   }
   sum = warp_sum(sum);
   const float logsum = logf(sum);
-  for (int k = lane; k < K; k += 32) {
-    const unsigned long long key = keys[warp][k];
+#pragma unroll
+  for (int k = lane; k < P; k += 32) {
+    if (k >= K) break;
+    const unsigned long long key = keys[k];
     const int id = (int)(key >> 32);
     const bool on = has && id != kNoId;
-    const float t = on ? teacher[n * K + (unsigned)key] * inv_t - m : 0.f;
+    const float t = on ? ts[(unsigned)key] - m : 0.f;
     sid[n * K + k] = on ? id : kNoId;
     sq[n * K + k] = on ? expf(t) / sum : 0.f;
     slogq[n * K + k] = on ? t - logsum : 0.f;
   }
   if (lane == 0) some[n] = has ? 1.f : 0.f;
+}
+cudaError_t teacher_prep(const int32_t* ids, const float* teacher, int N, int K, int V, float inv_t, int32_t* sid,
+                         float* sq, float* slogq, float* some, cudaStream_t st) {
+  const dim3 grid((unsigned)((N + 3) / 4)), block(128);
+  const auto kernel = K <= 32    ? teacher_prep_kernel<32>
+                      : K <= 64  ? teacher_prep_kernel<64>
+                      : K <= 128 ? teacher_prep_kernel<128>
+                                 : teacher_prep_kernel<256>;
+  return launch_pdl(kernel, grid, block, 0, st, ids, teacher, N, K, V, inv_t, sid, sq, slogq, some);
 }
 
 // ------------------------------------------------------------------ rows
@@ -440,10 +455,21 @@ __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
     if (a.acc) {
       float* p = a.acc + i * a.N + col;
       const int cols = min(8, a.N - col);
-      if (a.acc_in)
-        for (int j = 0; j < cols; ++j) s[j] += p[j];
+      const bool whole = cols == 8 && a.N % 4 == 0;
+      if (a.acc_in) {
+        if (whole) {
+          float old[8];
+          load8(p, old);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] += old[j];
+        } else {
+          for (int j = 0; j < cols; ++j) s[j] += p[j];
+        }
+      }
       if (a.acc_out) {
-        for (int j = 0; j < cols; ++j) p[j] = s[j];
+        if (whole) store8(p, s);
+        else
+          for (int j = 0; j < cols; ++j) p[j] = s[j];
         continue;
       }
     }
@@ -826,7 +852,7 @@ Layout layout(const VocabLoss& p, int backward) {
   L.planes = !f32 ? 1 : backward ? 3 : 0;
   L.terms = f32 ? 3 : 1;
   L.rows = round_up(std::max(p.N, 1), 256);
-  L.ld = round_up(p.d, 8);
+  L.ld = round_up(p.d, 64);  // rows on 128-byte lines
   const size_t n = (size_t)p.N;
   if (p.teacher) {
     L.sid = take(n * p.K * 4);
@@ -838,7 +864,10 @@ Layout layout(const VocabLoss& p, int backward) {
   // A forward pass over one row tile has nothing to gain from leaving rows
   // out, and its rows do not mix: it reads h where it is.
   L.gather = !L.few && (f32 || backward || p.N > BM || !tma_ready(p.h, p.ld_h));
-  L.pack_w = !L.few && (f32 || !tma_ready(p.w, p.ld_w));
+  // w is copied where TMA cannot read it, and where its rows do not start on
+  // 128-byte lines and enough rows of h use it: such rows cost 27 % of the
+  // contraction's rate (V = 32003, d = 1000), the copy about 20 us.
+  L.pack_w = !L.few && (f32 || !tma_ready(p.w, p.ld_w) || (p.N >= 2048 && p.ld_w % 64 != 0));
   if (L.gather) {
     L.row_of = take(n * 4);
     L.count = take(4);
@@ -903,8 +932,7 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
   if (p.teacher) {
     int32_t* sid = at<int32_t>(ws, L.sid);
     float *sq = at<float>(ws, L.sq), *slogq = at<float>(ws, L.slogq), *some = at<float>(ws, L.some);
-    VOCAB_TRY(launch_pdl(teacher_prep_kernel, dim3((unsigned)((p.N + 3) / 4)), dim3(128), 0, st, p.ids, p.teacher, p.N,
-                         p.K, p.V, p.inv_t, sid, sq, slogq, some));
+    VOCAB_TRY(teacher_prep(p.ids, p.teacher, p.N, p.K, p.V, p.inv_t, sid, sq, slogq, some, st));
     r->list = RowList{sid, sq, some, p.K};
     r->slogq = slogq;
   }
