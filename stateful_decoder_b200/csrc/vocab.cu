@@ -426,10 +426,11 @@ __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
   const int tile_rows = BM * a.cg;
   Cut cut;
   cut.init(M, a.N, K, tile_rows, a.bn, a.terms, a.units, a.max_splits);
-  const int total = cut.rest * tile_rows * (BN / 8), tile = tile_rows * (BN / 4);
+  const int rows = min(M, tile_rows);  // of a tile, that exist
+  const int total = cut.rest * rows * (BN / 8), tile = tile_rows * (BN / 4);
   const int64_t stride = (int64_t)cut.rest * tile;
   for (int e = (int)blockIdx.x * 256 + threadIdx.x; e < total; e += (int)gridDim.x * 256) {
-    const int row = e % tile_rows, c = e / tile_rows % (BN / 8) * 8, rest = e / (tile_rows * (BN / 8));
+    const int row = e % rows, c = e / rows % (BN / 8) * 8, rest = e / (rows * (BN / 8));
     int m, nt;
     cut.place(cut.whole + rest, kPanel / a.cg, &m, &nt);
     const int64_t i = (int64_t)m * tile_rows + row;
@@ -586,11 +587,11 @@ __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld
 #pragma unroll 2
   for (int it = 0; it < total; ++it) {
     if (vec && it + 1 < total) fetch(nxt);
+    if (vec) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = step * (32 * U) + u * 32 + lane;
-      if (c >= d8) continue;
-      if (vec && c * 8 + 8 <= d) {
+      for (int u = 0; u < U; ++u) {
+        const int c = step * (32 * U) + u * 32 + lane;
+        if (c * 8 + 8 > d) continue;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const float4 lo = hs[(b * 2) * d8 + c], hi = hs[(b * 2 + 1) * d8 + c];
@@ -608,16 +609,29 @@ __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld
             t = fmaf(x.get(7), hi.w, t);
           }
         }
-      } else {
-        const float* hf = reinterpret_cast<const float*>(hs);
-        for (int j = 0; j < 8 && c * 8 + j < d; ++j) {
+      }
+    }
+    // rows off the 16-byte grid, and the last columns of the others: element
+    // by element, the lanes side by side
+    const float* hf = reinterpret_cast<const float*>(hs);
+    const int k_end = min(d, (step + 1) * 256 * U);
+    for (int k0 = vec ? max(step * 256 * U, d / 8 * 8) : step * 256 * U; k0 < k_end; k0 += 128) {
+      float y[4][R];
 #pragma unroll
-          for (int i = 0; i < R; ++i) {
-            const float y = to_f32(w[min(v0 + i, (int64_t)V - 1) * ld_w + c * 8 + j]);
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-              acc[i * NB + b] = fmaf(y, hf[((b * 2 + (j >> 2)) * d8 + c) * 4 + (j & 3)], acc[i * NB + b]);
-          }
+        for (int i = 0; i < R; ++i) {
+          const int k = k0 + u * 32 + lane;
+          y[u][i] = k < k_end ? to_f32(w[min(v0 + i, (int64_t)V - 1) * ld_w + k]) : 0.f;
+        }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = min(k0 + u * 32 + lane, d - 1);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float hk = hf[((b * 2 + ((k >> 2) & 1)) * d8 + (k >> 3)) * 4 + (k & 3)];
+#pragma unroll
+          for (int i = 0; i < R; ++i) acc[i * NB + b] = fmaf(y[u][i], hk, acc[i * NB + b]);
         }
       }
     }
@@ -993,13 +1007,25 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
                  : launch_pdl(gather_kernel<float>, grid, dim3(256), 0, st, g);
 }
 
+// k-blocks per tensor-memory sum.  bf16: 16, an error of the logits of some
+// 1e-6 of themselves, far below their operands' rounding.  fp32: 4, and fewer
+// where a product has no more than a round of tiles and the extra sums are not
+// what it waits for (a logit of 15 off by 12 steps of 2^-21 moved a
+// probability, and so a gradient, by 5e-6).
+int chunk_of(int dtype, int64_t M, int64_t N, int bn, int single) {
+  if (dtype) return 16;
+  const int cg = cta_group((int)M);
+  const int64_t tiles = (M + BM * cg - 1) / (BM * cg) * ((N + bn - 1) / bn);
+  return tiles <= kSmCount / cg ? single : 4;
+}
+
 Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
   Args a{};
   a.terms = L.terms;
+  a.chunk = 4;
   a.fp16 = p.dtype == 0;
   a.h_inv = r.h_inv;
   a.w_inv = r.w_inv;
-  a.chunk = p.dtype ? 16 : 4;
   a.bn = BN;
   a.max_splits = 1;
   a.list = r.list;
@@ -1043,13 +1069,15 @@ cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a
   a.accumulate = accumulate;
   a.vec = vector_rows(out, ld, p.dtype);
   // bf16 gradients: a sum's drift over 4096 of k (8e-6) is far below their own rounding
-  if (p.dtype) a.chunk = 64;
+  a.chunk = p.dtype ? 64 : chunk_of(0, a.M, a.N, a.bn, 2);
   VOCAB_TRY(contract<KIND>(G, B, nullptr, a, st));
   if (a.max_splits == 1) return cudaSuccess;
   const SlabSum s{slab,    a.M,          a.N, a.K,      a.m_count, a.k_count, a.terms,
                   a.units, a.max_splits, cg, a.bn, a.row_of, out,       ld,        accumulate, a.vec,
                   a.acc,   a.acc_in,     a.acc_out};
-  const dim3 grid((unsigned)std::min<int64_t>(4 * kSmCount, ((int64_t)a.M * a.N + 2047) / 2048));
+  const int64_t tiles = (a.M + BM * cg - 1) / (BM * cg) * (int64_t)((a.N + a.bn - 1) / a.bn);
+  const int64_t most = std::min<int64_t>(tiles, a.units) * std::min(a.M, BM * cg) * (BN / 8);
+  const dim3 grid((unsigned)std::min<int64_t>(4 * kSmCount, (most + 255) / 256));
   return p.dtype ? launch_pdl(slab_sum_kernel<bf16>, grid, dim3(256), 0, st, s)
                  : launch_pdl(slab_sum_kernel<float>, grid, dim3(256), 0, st, s);
 }
@@ -1074,6 +1102,7 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
     a.N = p.V;
     a.K = p.d;
     a.bn = L.bn;
+    a.chunk = chunk_of(p.dtype, p.N, p.V, L.bn, 1);
     // The list kernel before this one let it start after its own wait, so h
     // and w are complete: only the epilogue waits for the lists.
     a.early = p.teacher != nullptr && !L.gather && !L.pack_w;
@@ -1110,6 +1139,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.lse = lse;
     a.weight = weight;
     a.bn = L.bn;
+    a.chunk = chunk_of(p.dtype, p.N, width, L.bn, 1);
     VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(r.zh, r.zw, &G, a, st)
               : L.g_planes == 2 ? contract<GRAD2>(r.zh, r.zw, &G, a, st)
                                 : contract<GRAD3>(r.zh, r.zw, &G, a, st));

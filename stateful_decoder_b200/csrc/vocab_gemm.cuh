@@ -381,12 +381,14 @@ __device__ __forceinline__ void stats_epilogue(const Args& a, int64_t i, int64_t
 #pragma unroll
     for (int j = 0; j < 32; ++j) m = fmaxf(m, x[c][j]);
   }
-  const float sub = m > -INFINITY ? m * s2 : 0.f;
+  // (x - m) first: one product of x less one of m would round at the size of
+  // the logits, 1e-6 of a sum at logits of 15
+  const float ref = m > -INFINITY ? m : 0.f;
   float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int j = 0; j < 32; ++j) t[j & 3] += ex2(fmaf(x[c][j], s2, -sub));
+    for (int j = 0; j < 32; ++j) t[j & 3] += ex2((x[c][j] - ref) * s2);
   if (on)
     a.part[(int64_t)(n_tile * 2 + half) * a.part_ld + i] =
         make_float2(m * a.scale, cols > 0 ? (t[0] + t[1]) + (t[2] + t[3]) : 0.f);
@@ -398,13 +400,12 @@ template <int PLANES>
 __device__ __forceinline__ void grad_epilogue(const Args& a, const CUtensorMap* tm, uint32_t stage, int64_t i0,
                                               int lane, int64_t n, bool on, int n_tile, int half, int v0, int pos,
                                               float (&x)[4][32]) {
-  const float s2 = a.scale * kLog2e;
   const int col0 = n_tile * a.bn + half * 128;
   const int cols = min(min(128, a.bn - half * 128), a.N - col0);
   // what is written: whole k-blocks of the products to come, zeros past N
   const int out_cols = min(min(128, a.bn - half * 128), (a.N + BK - 1) / BK * BK - col0);
   const float cw = on ? a.weight[n] * a.scale : 0.f;
-  const float sub = on ? a.lse[n] * kLog2e : 0.f;
+  const float l = on ? a.lse[n] : 0.f;
   int next = on && pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
   const uint32_t row = (uint32_t)lane * 64, sw = (uint32_t)(lane >> 1) & 3u;
 #pragma unroll
@@ -412,7 +413,7 @@ __device__ __forceinline__ void grad_epilogue(const Args& a, const CUtensorMap* 
     float* v = x[c];
     if (on) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = cw * ex2(fmaf(v[j], s2, -sub));
+      for (int j = 0; j < 32; ++j) v[j] = cw * ex2(fmaf(v[j], a.scale, -l) * kLog2e);
       while (next >= v0 + c * 32 && next < v0 + min(c * 32 + 32, cols)) {
         sub_at(v, next - v0 - c * 32, cw * (a.list.q ? a.list.q[n * a.list.K + pos] : 1.f));
         next = ++pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
