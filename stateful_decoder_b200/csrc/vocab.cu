@@ -497,14 +497,16 @@ __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
 // products) and h through shared memory, in fp32.  A warp takes two to four
 // rows of w at a time against all NB rows of h; the sums of its lanes are added by
 // exchanging halves, after which lane r * NB + n holds z of w row r and h row n.
-// At V = 32000, d = 2048, one row: 28 us, where the tensor-core path takes 42:
-// there every SM asks L2 for the same 128 bytes of h at a time.
+// At V = 32000, d = 2048: bf16 29, 31, 39 and 56 us for 1, 2, 4 and 8 rows
+// against 33 on the tensor cores, so up to 2; fp32 53 and 79 us for 4 and 8
+// against 165 (there w is first split into planes), so up to 8.
 // Rows of w per group: few, so that the groups spread evenly over the warps
 // (at V = 32000 four per group leave a round 38 % full), but four where each
 // read of h from shared memory has to serve more products.
 template <int NB>
 constexpr int kFewW = NB <= 2 ? 2 : 4;
 constexpr int kFewRows = 8;
+int few_rows_limit(int dtype) { return dtype ? 2 : kFewRows; }
 constexpr size_t kFewSmem = 200 << 10;  // h in shared memory
 
 template <typename T>
@@ -822,17 +824,17 @@ int64_t slab_floats(int64_t M, int64_t N, int64_t kblocks, int* most) {
 }
 
 // Columns per tile of the logits: the width whose rounds take the least time,
-// a tile costing its columns and some more for its rows' operand (128 where
-// the tensor cores are the limit: 192 columns ran at 0.87 of the rate of 256;
-// 64 where reading w is).  Narrow tiles where one round would leave SMs idle.
-// (The gradient writes 64 columns at a time.)
-int logit_columns(int64_t M, int64_t V, int backward) {
+// a tile costing its columns and 128 more for its rows' operand and what is
+// fixed (192 columns ran at 0.87 of the rate of 256).  Wide tiles where there
+// are many, narrow ones where wide ones leave the last round's SMs idle: 501
+// fp32 rows at V = 32000, d = 512, forward and backward, 415 us for 460.
+int logit_columns(int64_t M, int64_t V) {
   const int cg = cta_group((int)M);
   const int64_t units = kSmCount / cg, m_tiles = (M + BM * cg - 1) / (BM * cg);
   int best = BN;
   int64_t cost = INT64_MAX;
-  for (int bn = BN; bn >= 64; bn -= backward || cg == 2 ? 64 : 32) {
-    const int64_t c = (m_tiles * ((V + bn - 1) / bn) + units - 1) / units * (bn + (m_tiles > 1 ? 128 : 64));
+  for (int bn = BN; bn >= 64; bn -= 64) {  // the gradient writes 64 columns at a time
+    const int64_t c = (m_tiles * ((V + bn - 1) / bn) + units - 1) / units * (bn + 128);
     if (c < cost) {
       cost = c;
       best = bn;
@@ -840,7 +842,9 @@ int logit_columns(int64_t M, int64_t V, int backward) {
   }
   return best;
 }
-// Columns per tile of a product with d columns (its idle SMs take ranges of K).
+// Columns per tile of a product with d columns (its idle SMs take ranges of
+// K): fewer than 256 where d does not fill them, 2 to 8 % of a backward at
+// d = 64 to 300.
 int product_columns(int64_t M, int64_t d) {
   const int step = 64 * cta_group((int)M);
   int best = BN;
@@ -853,6 +857,18 @@ int product_columns(int64_t M, int64_t d) {
     }
   }
   return best;
+}
+
+// Time of a product in k-blocks of a round: its whole rounds, and the last one
+// as split_rule cuts it.
+int64_t product_time(int64_t M, int64_t N, int64_t kblocks) {
+  const int cg = cta_group((int)M), bn = product_columns(M, N), units = kSmCount / cg;
+  const int64_t tiles = (M + BM * cg - 1) / (BM * cg) * ((N + bn - 1) / bn);
+  const int left = (int)(tiles % units), s = left ? split_rule(left, units, (int)kblocks, kMostSplits) : 1;
+  const int64_t rest = !left ? 0
+                       : s == 1 ? kblocks
+                                : (left * s + units - 1) / units * ((kblocks + s - 1) / s + 12) + 12;
+  return tiles / units * kblocks + rest;
 }
 
 Layout layout(const VocabLoss& p, int backward) {
@@ -874,14 +890,14 @@ Layout layout(const VocabLoss& p, int backward) {
     L.slogq = take(n * p.K * 4);
     L.some = take(n * 4);
   }
-  L.few = !backward && p.N <= kFewRows && (size_t)kFewRows * round_up(p.d, 8) * 4 <= kFewSmem;
+  L.few = !backward && p.N <= few_rows_limit(p.dtype) && (size_t)kFewRows * round_up(p.d, 8) * 4 <= kFewSmem;
   // A forward pass over one row tile has nothing to gain from leaving rows
   // out, and its rows do not mix: it reads h where it is.
   L.gather = !L.few && (f32 || backward || p.N > BM || !tma_ready(p.h, p.ld_h));
-  // w is copied where TMA cannot read it, and where its rows do not start on
-  // 128-byte lines and enough rows of h use it: such rows cost 27 % of the
-  // contraction's rate (V = 32003, d = 1000), the copy about 20 us.
-  L.pack_w = !L.few && (f32 || !tma_ready(p.w, p.ld_w) || (p.N >= 2048 && p.ld_w % 64 != 0));
+  // w is read where it is whenever TMA can: rows that do not start on 128-byte
+  // lines cost up to 27 % of a contraction's rate (d = 1000), but a copy on
+  // every call costs more (2048 rows, V = 32000: 107 us with it, 94 without).
+  L.pack_w = !L.few && (f32 || !tma_ready(p.w, p.ld_w));
   if (L.gather) {
     L.row_of = take(n * 4);
     L.count = take(4);
@@ -895,7 +911,7 @@ Layout layout(const VocabLoss& p, int backward) {
     L.w_inv = take((size_t)(round_up(p.V, BN) + BN) * 4);  // tiles read past V
   }
   const int64_t n_tiles = (p.V + BN - 1) / BN;
-  L.bn = logit_columns(p.N, p.V, backward);
+  L.bn = logit_columns(p.N, p.V);
   if (!backward) {
     L.parts = L.few ? (int)std::min<int64_t>(kSmCount, (p.V + 15) / 16) : 2 * ((p.V + L.bn - 1) / L.bn);
     L.part = take((size_t)L.parts * (L.few ? kFewRows : L.rows) * 8);
@@ -903,17 +919,30 @@ Layout layout(const VocabLoss& p, int backward) {
     return L;
   }
   // g of bf16 operands is rounded to bf16 as an operand of the products, about
-  // as much again as the gradients' own rounding.  Up to 256 rows a second
-  // plane costs next to nothing (the products are bound by w and dw) and
-  // leaves their own rounding alone.
+  // as much again as the gradients' own rounding (1.41 of it in all, over many
+  // rows).  Over few rows single entries of g carry the gradients and their
+  // rounding does not average: up to 256 rows a second plane takes it away, at
+  // 13 to 22 % of the backward's time (64 to 256 rows, V = 32000, d = 2048).
   L.g_planes = f32 ? 3 : p.N <= 256 ? 2 : 1;
   L.g_terms = f32 ? 6 : L.g_planes;
-  // The piece: as wide as 512 MB of g allow, at least 2048 columns; equal pieces.
+  // The piece: at most as wide as 512 MB of g allow (256 MB was 5 % slower at
+  // 16,368 rows, 1 GB no faster), at least 2048 columns, and of the next few
+  // equal cuts the one whose products fill their rounds best.
   const int64_t most = std::max<int64_t>(2048, ((int64_t)512 << 20) / (L.rows * 2 * L.g_planes) / BN * BN);
-  const int64_t whole = n_tiles * BN;
-  L.pieces = (int)((whole + most - 1) / most);
-  L.piece = (int)round_up((whole + L.pieces - 1) / L.pieces, BN);
-  L.pieces = (int)((whole + L.piece - 1) / L.piece);
+  const int64_t whole = n_tiles * BN, fewest = (whole + most - 1) / most;
+  int64_t best = INT64_MAX;
+  for (int64_t q = fewest; q < fewest + 3; ++q) {
+    const int64_t piece = round_up((whole + q - 1) / q, BN);
+    if (q > fewest && piece < 2048) break;
+    const int64_t pieces = (whole + piece - 1) / piece;
+    const int64_t cost = pieces * (product_time(p.N, p.d, piece / BK * L.g_terms) +
+                                   product_time(piece, p.d, L.rows / BK * L.g_terms) + 32);
+    if (cost < best) {
+      best = cost;
+      L.piece = (int)piece;
+      L.pieces = (int)pieces;
+    }
+  }
   L.g = take((size_t)L.g_planes * L.rows * L.piece * 2);
   L.dw = take((size_t)slab_floats(L.piece, p.d, L.rows / BK * L.g_terms, &L.dw_splits) * 4);
   L.dh = take((size_t)slab_floats(p.N, p.d, (int64_t)L.piece / BK * L.g_terms, &L.dh_splits) * 4);
@@ -1007,16 +1036,16 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
                  : launch_pdl(gather_kernel<float>, grid, dim3(256), 0, st, g);
 }
 
-// k-blocks per tensor-memory sum.  bf16: 16, an error of the logits of some
-// 1e-6 of themselves, far below their operands' rounding.  fp32: 4, and fewer
-// where a product has no more than a round of tiles and the extra sums are not
-// what it waits for (a logit of 15 off by 12 steps of 2^-21 moved a
-// probability, and so a gradient, by 5e-6).
-int chunk_of(int dtype, int64_t M, int64_t N, int bn, int single) {
+// k-blocks per tensor-memory sum of the logits.  bf16: 16, an error of some
+// 1e-6 of a logit, far below its operands' rounding.  fp32: 4, and 1 where the
+// tiles are no more than a round and the extra sums are not what they wait for
+// (a logit of 15 off by 12 steps of 2^-21 moved a probability, and so a
+// gradient, by 5e-6).  For longer work 1 would cost 10 %.
+int logit_chunk(int dtype, int64_t M, int64_t N, int bn) {
   if (dtype) return 16;
   const int cg = cta_group((int)M);
   const int64_t tiles = (M + BM * cg - 1) / (BM * cg) * ((N + bn - 1) / bn);
-  return tiles <= kSmCount / cg ? single : 4;
+  return tiles <= kSmCount / cg ? 1 : 4;
 }
 
 Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
@@ -1046,13 +1075,13 @@ cudaError_t few_rows(const VocabLoss& p, const Layout& L, const RowList& list, f
                     (int)(p.teacher != nullptr), part,
                     (int64_t)kFewRows, zsel);
 }
-template <typename T>
 cudaError_t few_rows_of(const VocabLoss& p, const Layout& L, const RowList& list, float2* part, float* zsel,
                         cudaStream_t st) {
-  if (p.N == 1) return few_rows<T, 1>(p, L, list, part, zsel, st);
-  if (p.N == 2) return few_rows<T, 2>(p, L, list, part, zsel, st);
-  if (p.N <= 4) return few_rows<T, 4>(p, L, list, part, zsel, st);
-  return few_rows<T, 8>(p, L, list, part, zsel, st);
+  if (p.dtype) return p.N == 1 ? few_rows<bf16, 1>(p, L, list, part, zsel, st) : few_rows<bf16, 2>(p, L, list, part, zsel, st);
+  if (p.N == 1) return few_rows<float, 1>(p, L, list, part, zsel, st);
+  if (p.N == 2) return few_rows<float, 2>(p, L, list, part, zsel, st);
+  if (p.N <= 4) return few_rows<float, 4>(p, L, list, part, zsel, st);
+  return few_rows<float, 8>(p, L, list, part, zsel, st);
 }
 
 // A product of g into typed rows, K split where the rule says so.
@@ -1069,7 +1098,7 @@ cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a
   a.accumulate = accumulate;
   a.vec = vector_rows(out, ld, p.dtype);
   // bf16 gradients: a sum's drift over 4096 of k (8e-6) is far below their own rounding
-  a.chunk = p.dtype ? 64 : chunk_of(0, a.M, a.N, a.bn, 2);
+  a.chunk = p.dtype ? 64 : 4;
   VOCAB_TRY(contract<KIND>(G, B, nullptr, a, st));
   if (a.max_splits == 1) return cudaSuccess;
   const SlabSum s{slab,    a.M,          a.N, a.K,      a.m_count, a.k_count, a.terms,
@@ -1094,7 +1123,7 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
   float2* part = at<float2>(ws, L.part);
   float* zsel = at<float>(ws, L.zsel);
   if (L.few) {
-    VOCAB_TRY((p.dtype ? few_rows_of<bf16> : few_rows_of<float>)(p, L, r.list, part, zsel, st));
+    VOCAB_TRY(few_rows_of(p, L, r.list, part, zsel, st));
   } else {
     Args a = args_of(p, L, r);
     a.M = p.N;
@@ -1102,7 +1131,7 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
     a.N = p.V;
     a.K = p.d;
     a.bn = L.bn;
-    a.chunk = chunk_of(p.dtype, p.N, p.V, L.bn, 1);
+    a.chunk = logit_chunk(p.dtype, p.N, p.V, L.bn);
     // The list kernel before this one let it start after its own wait, so h
     // and w are complete: only the epilogue waits for the lists.
     a.early = p.teacher != nullptr && !L.gather && !L.pack_w;
@@ -1139,7 +1168,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.lse = lse;
     a.weight = weight;
     a.bn = L.bn;
-    a.chunk = chunk_of(p.dtype, p.N, width, L.bn, 1);
+    a.chunk = logit_chunk(p.dtype, p.N, width, L.bn);
     VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(r.zh, r.zw, &G, a, st)
               : L.g_planes == 2 ? contract<GRAD2>(r.zh, r.zw, &G, a, st)
                                 : contract<GRAD3>(r.zh, r.zw, &G, a, st));
