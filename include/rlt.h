@@ -449,12 +449,14 @@ int32_t rlt_op_sample(const float* logits_dev, int32_t B, int32_t V, const rlt_s
 
 /* Operands of the loss over the vocabulary: N rows of h (a readout operand,
  * report eq. 2.6) against the V rows of w (a readout or embedding matrix),
- * both row-major in `dtype` with rows ld_* elements apart (ld >= d).  Any N,
- * V, d and row distance; 0 <= N, 1 <= V, 1 <= d.  Fastest where the bases are
- * 16-byte aligned and (bf16) ld % 8 == 0; other bf16 operands are repacked.
- * The logits are
+ * both row-major in `dtype` with rows ld_* elements apart (ld >= d), finite.
+ * Any N >= 0, V >= 1, d >= 1 up to 2^28 and any row distance; bf16 operands
+ * whose base is not 16-byte aligned or whose ld % 8 != 0 are copied into the
+ * workspace first.  The logits are
  *   z[n][v] = sum_k h[n][k] w[v][k],
- * accumulated in fp32.  They are formed a piece of the vocabulary at a time and never kept. */
+ * accumulated in fp32 (fp32 operands to fp32 accuracy, on the tensor cores in
+ * 16-bit parts).  They are formed a piece of the vocabulary at a time and
+ * never kept. */
 typedef struct rlt_vocab {
   const void* h;     /* [N][d], device */
   int64_t ld_h;
@@ -487,7 +489,9 @@ int32_t rlt_op_cross_entropy(const rlt_vocab* a, const int32_t* target_dev, floa
  * (zeros for rows without a target or of weight 0, whose h is not used);
  * dw_dev [V][d] is written whole or, with accumulate_dw, added to.  Either
  * may be NULL, not both; neither may overlap an operand.  Sums are fp32; with
- * bf16 operands dz is rounded to bf16 once, as an operand of the two products.
+ * bf16 operands dz is rounded to bf16 once, as an operand of the two products
+ * (to 16 bits for up to 256 rows).  The workspace holds up to 512 MB of dz, or
+ * 2048 columns of it where that is more.
  * Errors: as rlt_op_cross_entropy. */
 int32_t rlt_op_cross_entropy_backward(const rlt_vocab* a, const int32_t* target_dev, const float* lse_dev,
                                       const float* weight_dev, void* dh_dev, int64_t ld_dh, void* dw_dev,

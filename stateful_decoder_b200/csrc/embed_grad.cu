@@ -11,8 +11,8 @@
 // in registers, writes the rows of ids that begin and end inside it, and
 // leaves an fp32 partial for the id that it shares with its neighbours; the
 // partials are added in run order.  demb is zeroed by the SMs that have no part
-// in the sort, while it runs (rows that are then written again cost less than
-// finding the absent ones afterwards: 205 us became 190 at N = 65,536).  Bound by the bytes of
+// in the sort, while it runs (finding the absent rows afterwards took as long at
+// N = 65,536 and 16 us more at N = 8,191, d = 512).  Bound by the bytes of
 // dout and demb, each moved once; nothing is added atomically.
 #include <algorithm>
 
@@ -510,8 +510,9 @@ Layout layout(int N, int V, int d) {
   };
   if (N == 0) return L;
   while (L.passes < 4 && ((uint64_t)V >> (8 * L.passes)) != 0) ++L.passes;  // keys 0..V
-  // Longer runs leave fewer partials, shorter ones more groups: 16 rows keep
-  // the SMs busy from a few thousand rows on, 64 cost 3 % of the traffic.
+  // Longer runs leave fewer partials, shorter ones more groups to work.  Lookup
+  // and gradient at d = 2048 with runs of 16 and of 64: 44 and 59 us for 1,000
+  // rows, 70 and 78 for 8,191, 93 and 90 for 16,384, 233 and 205 for 65,536.
   L.run = N <= kSortOne ? 16 : 64;
   L.runs = ((int64_t)N + L.run - 1) / L.run;
   L.group = 32;

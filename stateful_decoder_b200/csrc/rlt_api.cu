@@ -1855,6 +1855,12 @@ namespace {
 
 bool known_dtype(int32_t t) { return t == RLT_DTYPE_F32 || t == RLT_DTYPE_BF16; }
 
+// Extents the kernels' 32-bit row and column numbers hold with room to spare.
+constexpr int32_t kMaxExtent = 1 << 28;
+bool extents(int32_t N, int32_t V, int32_t d) {
+  return N >= 0 && V >= 1 && d >= 1 && N <= kMaxExtent && V <= kMaxExtent && d <= kMaxExtent;
+}
+
 // The workspace convention: reports the size (returns 1 with ws null), or checks it.
 int32_t check_workspace(void* ws, size_t* ws_bytes, size_t need, bool* report) {
   *report = ws == nullptr;
@@ -1872,8 +1878,8 @@ int32_t check_workspace(void* ws, size_t* ws_bytes, size_t need, bool* report) {
 int32_t vocab_problem(const rlt_vocab* a, const int32_t* ids, const float* teacher, int32_t K, float temperature,
                       const size_t* ws_bytes, VocabLoss* p) {
   if (!a || !ws_bytes) return fail(RLT_E_INVAL, "null operands or workspace size");
-  if (a->N < 0 || a->V < 1 || a->d < 1 || a->ld_h < a->d || a->ld_w < a->d)
-    return fail(RLT_E_INVAL, "vocabulary operands need N >= 0, V >= 1, d >= 1 and ld >= d");
+  if (!extents(a->N, a->V, a->d) || a->ld_h < a->d || a->ld_w < a->d)
+    return fail(RLT_E_INVAL, "vocabulary operands need N >= 0, V >= 1, d >= 1, none over 2^28, and ld >= d");
   if (!known_dtype(a->dtype)) return fail(RLT_E_INVAL, "dtype");
   if (!a->w || (a->N > 0 && (!a->h || !ids))) return fail(RLT_E_INVAL, "null operand");
   if (K < 1 || K > 256) return fail(RLT_E_INVAL, "1 <= K <= 256");
@@ -1948,7 +1954,7 @@ int32_t rlt_op_distill_backward(const rlt_vocab* a, const int32_t* ids_dev, cons
 int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int32_t V, int32_t d,
                      const int32_t* tok_dev, int32_t N, float scale, void* out_dev, int64_t ld_out,
                      int32_t out_dtype, void* stream) {
-  if (N < 0 || V < 1 || d < 1 || ld_emb < d || ld_out < d || !emb_dev || (N > 0 && (!tok_dev || !out_dev)))
+  if (!extents(N, V, d) || ld_emb < d || ld_out < d || !emb_dev || (N > 0 && (!tok_dev || !out_dev)))
     return fail(RLT_E_INVAL, "bad embedding arguments");
   if (!known_dtype(emb_dtype) || !known_dtype(out_dtype)) return fail(RLT_E_INVAL, "dtype");
   RLT_CUDA(embed_lookup(emb_dev, ld_emb, emb_dtype, V, d, tok_dev, N, scale, out_dev, ld_out, out_dtype,
@@ -1959,7 +1965,7 @@ int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int
 int32_t rlt_op_embed_backward(const void* dout_dev, int64_t ld_dout, int32_t dout_dtype, const int32_t* tok_dev,
                               int32_t N, int32_t V, int32_t d, float scale, void* demb_dev, int64_t ld_demb,
                               int32_t demb_dtype, int32_t accumulate, void* ws_dev, size_t* ws_bytes, void* stream) {
-  if (N < 0 || V < 1 || d < 1 || ld_dout < d || ld_demb < d || !demb_dev || !ws_bytes ||
+  if (!extents(N, V, d) || ld_dout < d || ld_demb < d || !demb_dev || !ws_bytes ||
       (N > 0 && (!tok_dev || !dout_dev)))
     return fail(RLT_E_INVAL, "bad embedding gradient arguments");
   if (!known_dtype(dout_dtype) || !known_dtype(demb_dtype)) return fail(RLT_E_INVAL, "dtype");

@@ -5,8 +5,8 @@
 //   D[m][n] = sum over terms and k of A[plane a][m][k] B[plane b][n][k]
 //
 // Kinds:
-//   STATS  D = h w^T: per row and 128 columns, the maximum and the sum of
-//          exponentials of z = D * inv_t, and z at the row's listed ids
+//   STATS  D = h w^T: per row and up to 128 columns, the maximum and the sum
+//          of exponentials of z = D * inv_t, and z at the row's listed ids
 //   GRAD   D = h w^T: g = c (exp(z - lse) - q), rounded to bf16
 //   GRAD2, GRAD3  the same as two or three bf16 planes whose sum is g to
 //          2^-16 or 2^-24
@@ -31,6 +31,13 @@
 // So a sum stays in tensor memory for `chunk` k-blocks only; the epilogue
 // warps add the chunks in registers, rounding to nearest, under the next
 // chunk's MMAs.
+//
+// Bound by the tensor cores where there are rows enough: at 8,192 rows, V =
+// 32000, d = 2048, the tensor pipe is active 94 to 95 % of the time in all four
+// kinds and the power limit sets the clock (1.35 to 1.42 GHz): 655 us for
+// STATS, 1.64 PFLOP/s, and 1.54 to 1.59 in the others.  Two CTAs per tile
+// (256 x 256, each loads half of the columns' operand) took 8 % off a forward
+// and backward of 16,368 rows against one (128 x 256).
 #pragma once
 #include <cuda.h>
 
@@ -65,7 +72,7 @@ struct Args {
   int terms;              // 1, 2, 3 or 6 plane products
   int fp16;               // the operands' type: bf16 or fp16
   int chunk;              // k-blocks per tensor-memory sum (of the leading term)
-  int bn;                 // columns per tile: a multiple of 32 (GRAD: 64; DH, DW: 64 per CTA) up to BN
+  int bn;                 // columns per tile: a multiple of 64 (DH, DW: 64 per CTA) up to BN
   int stages;             // of bn's size
   int a_rows;             // rows of A that a tile loads (fewer than BM when M is: the rest are never looked at)
   int units;              // CTAs or pairs on the device
@@ -76,7 +83,6 @@ struct Args {
   RowList list;
   const float *h_inv, *w_inv;  // fp16 planes: 2^-e of the rows of h and w, or null
   const int32_t* row_of;  // compact row -> row, or null
-  int V;
   float scale;            // inv_t
   float2* part;           // [2 * n_tiles][part_ld]
   int64_t part_ld;
@@ -343,8 +349,9 @@ struct Plan : Cut {
 };
 
 // ---------------------------------------------------------------- epilogues
-// Each handles the 128 columns from n_tile * BN + half * 128 of one row per
+// Each handles up to 128 columns from n_tile * bn + half * 128 of one row per
 // thread, in registers.
+
 // Takes the operands' powers of two back; columns past the matrix are ignored
 // by what follows.
 __device__ __forceinline__ void unscale(const Args& a, int64_t i, bool on, int v0, float (&x)[4][32]) {
@@ -716,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if constexpr (KIND == STATS) stats_epilogue(a, i, n, on, tile.n, half, v0, pos, x);
       else if constexpr (KIND != DH && KIND != DW)
-        grad_epilogue<KIND == GRAD ? 1 : KIND == GRAD2 ? 2 : 3>(a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n,
-                                            on, tile.n, half, v0, pos, x);
+        grad_epilogue<KIND == GRAD ? 1 : KIND == GRAD2 ? 2 : 3>(
+            a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n, on, tile.n, half, v0, pos, x);
       else {
         float4* slab_row = tile.split < 0 ? nullptr
                                           : a.slab + ((int64_t)tile.split * plan.rest + tile.rest) * (BM * CG * BN / 4) +

@@ -182,12 +182,13 @@ def test_distill_matches_formula(env, N, V, d, K, T, dtype):
     rlt.rlt_check_device()
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_several_pieces_of_the_vocabulary(env, dtype):
+@pytest.mark.parametrize("N,dtype", [(90001, "bf16"), (90001, "f32"), (60000, "f32")])
+def test_several_pieces_of_the_vocabulary(env, N, dtype):
     """Many rows: the backward walks the vocabulary in more than one piece,
-    the last one short and odd."""
+    the last one short and odd; at 60,000 fp32 rows the last round of row
+    tiles is split over k as well."""
     rlt, torch = env
-    N, V, d = 90001, 5121, 16
+    V, d = 5121, 16
     h, w, target, weight = make(torch, N, V, d, dtype, seed=5)
     weight /= N
     got = ce(env, h, w, target, weight)
@@ -199,8 +200,59 @@ def test_several_pieces_of_the_vocabulary(env, dtype):
         for k in ("loss", "lse", "dh"):
             within(torch, got[k][s], ref[k], k)
         dw[0] = dw[0] + ref["dw"][0]
-        dw[1] = dw[1] + ref["dw"][1] * 7  # (2 n + 8) u counts all N terms
+        dw[1] = dw[1] + ref["dw"][1] * 7  # (2 n + 8) u counts all N terms (at most 6.01 times 15,000)
     within(torch, got["dw"], dw, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,d", [(2, 1000, 300), (3, 900, 61), (4, 5000, 520), (5, 70, 2100), (8, 3001, 130), (9, 640, 256),
+                                   (256, 900, 64), (257, 900, 64), (40, 20000, 192), (12, 251, 2432), (3000, 700, 74),
+                                   (300, 4000, 264)])
+def test_each_way_of_cutting_the_work(env, N, V, d, dtype):
+    """Few rows (streamed, and just past that), one and two planes of the logit
+    gradient, long sums split over the SMs with few and many tiles, narrow
+    tiles; with a list that has the target in it, at half temperature."""
+    rlt, torch = env
+    h, w, target, weight = make(torch, N, V, d, dtype, seed=N + d, ignored=0.1 if N > 8 else 0.0)
+    ids, teacher = make_list(torch, N, V, 6, seed=N)
+    got = ce(env, h, w, target, weight)
+    ref = reference(torch, h, w, target=target, weight=weight)
+    for k in ("loss", "lse", "dh", "dw"):
+        within(torch, got[k], ref[k], k)
+    got = kl(env, h, w, ids, teacher, 0.5, weight)
+    ref = reference(torch, h, w, T=0.5, ids=ids, teacher=teacher, weight=weight)
+    for k in ("loss", "lse", "dh", "dw"):
+        within(torch, got[k], ref[k], k)
+    rlt.rlt_check_device()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_few_of_many_rows_take_part(env, dtype):
+    """The work is cut by the rows that have a target, a count only the device
+    knows: one in a hundred, in runs and alone, first and last among them."""
+    rlt, torch = env
+    N, V, d = 5000, 3000, 136
+    h, w, target, weight = make(torch, N, V, d, dtype, seed=8, ignored=0.99)
+    target[0], target[N - 1], target[1200:1210] = 5, 2999, 7
+    got = ce(env, h, w, target, weight)
+    ref = reference(torch, h, w, target=target, weight=weight)
+    for k in ("loss", "lse", "dh", "dw"):
+        within(torch, got[k], ref[k], k)
+
+
+def test_few_rows_off_the_grid(env):
+    """Up to eight rows whose operands are not 16-byte aligned."""
+    rlt, torch = env
+    for dtype in ("bf16", "f32"):
+        for N in (1, 2, 7):
+            h, w, target, _ = make(torch, N, 333, 75, dtype, seed=N, ignored=0.0)
+            hb, wb = (torch.full((x.shape[0], 78), math.nan, dtype=x.dtype, device="cuda") for x in (h, w))
+            hb[:, 1:76], wb[:, 3:] = h, w
+            loss, lse = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+            rlt.rlt_op_cross_entropy(hb[:, 1:76], wb[:, 3:], target, loss, lse)
+            ref = reference(torch, h, w, target=target)
+            within(torch, loss, ref["loss"])
+            within(torch, lse, ref["lse"])
 
 
 def test_strided_and_misaligned_operands(env):
@@ -363,6 +415,35 @@ def test_side_stream_and_graph_replay(env):
         for got, eager in ((a, ce(env, h, w, target, weight)), (b, kl(env, h, w, ids, teacher, 0.8, weight))):
             for k in got:
                 assert torch.equal(got[k], eager[k]), k
+
+
+def test_streams_of_every_kind_and_two_calls_at_once(env):
+    """The legacy default stream by number and by object, and two calls at once
+    on two streams, each with the workspace that its call takes."""
+    rlt, torch = env
+    a = make(torch, 700, 3000, 128, "bf16", seed=1)
+    b = make(torch, 650, 2500, 192, "bf16", seed=2)
+    want = [ce(env, *x) for x in (a, b)]
+    torch.cuda.synchronize()
+    for stream in (0, torch.cuda.default_stream()):
+        got = ce(env, *a, stream=stream)
+        torch.cuda.synchronize()
+        for k in got:
+            assert torch.equal(got[k], want[0][k]), k
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [ce(env, *x, stream=s) for x, s in zip((a, b), streams)]
+        torch.cuda.synchronize()
+        for g, e in zip(got, want):
+            for k in g:
+                assert torch.equal(g[k], e[k]), k
+    tok = torch.randint(0, 3000, (700,), dtype=torch.int32).cuda()
+    grad = [torch.empty(3000, 128, device="cuda") for _ in range(2)]
+    rlt.rlt_op_embed_backward(a[0].float(), tok, grad[0])
+    torch.cuda.synchronize()
+    rlt.rlt_op_embed_backward(a[0].float(), tok, grad[1], stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(*grad)
 
 
 # ------------------------------------------------------------------ embedding

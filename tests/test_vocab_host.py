@@ -30,7 +30,8 @@ BIG = 1 << 40
 
 def test_operands_are_checked(rlt):
     lib = rlt._lib
-    for bad in (dict(N=-1), dict(V=0), dict(d=0), dict(ld_h=63), dict(ld_w=63), dict(dtype=2), dict(h=None), dict(w=None)):
+    for bad in (dict(N=-1), dict(V=0), dict(d=0), dict(ld_h=63), dict(ld_w=63), dict(dtype=2), dict(h=None), dict(w=None),
+                dict(N=(1 << 28) + 1), dict(V=(1 << 28) + 1), dict(d=(1 << 28) + 1, ld_h=1 << 29, ld_w=1 << 29)):
         a = ctypes.byref(operands(rlt, **bad))
         assert lib.rlt_op_cross_entropy(a, P, P, P, P, sized(BIG), None) == rlt.RLT_E_INVAL, bad
         assert lib.rlt_op_distill(a, P, P, 4, 1.0, P, P, P, sized(BIG), None) == rlt.RLT_E_INVAL, bad
