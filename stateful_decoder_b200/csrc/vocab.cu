@@ -120,23 +120,17 @@ __device__ __forceinline__ void planes8(bf16* dst, int64_t plane, int planes, fl
     for (int j = 0; j < 8; ++j) v[j] -= to_f32(from_f32<bf16>(v[j]));
   }
 }
-// 8 elements from column c of a row (zeros past d).
-template <typename T>
-__device__ __forceinline__ void row8(const T* row, int c, int d, bool vec, float* v) {
-  if (vec && c + 8 <= d) {
-    load8(row + c, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < d ? to_f32(row[c + j]) : 0.f;
-  }
-}
-// One row by a warp, several groups of eight in flight per lane.
+// One row by a warp, several loads in flight per lane: eight elements per lane
+// (single loads where a bf16 row is not 16-byte aligned: its copy is, and
+// 2-byte stores would cost more), or the lanes side by side for fp32.
 template <typename T>
 __device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out, int64_t plane, int planes) {
   const int lane = threadIdx.x & 31;
-  if constexpr (sizeof(T) == 2) {
-    if (vec) {  // one plane: the bits as they are
-      const int d8 = d / 8;
+  int done = 0;
+  if (vec) {
+    const int d8 = d / 8;
+    done = d8 * 8;
+    if constexpr (sizeof(T) == 2) {  // one plane: the bits as they are
       for (int c0 = lane; c0 < d8; c0 += 128) {
         uint4 v[4];
 #pragma unroll
@@ -146,58 +140,104 @@ __device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out,
         for (int u = 0; u < 4; ++u)
           if (c0 + u * 32 < d8) reinterpret_cast<uint4*>(out)[c0 + u * 32] = v[u];
       }
-      for (int c = d8 * 8 + lane; c < d; c += 32) out[c] = x[c];
-      return;
+    } else {
+      for (int c0 = lane; c0 < d8; c0 += 64) {
+        float v[2][8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (c0 + u * 32 < d8) load8(x + (c0 + u * 32) * 8, v[u]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (c0 + u * 32 < d8) planes8(out + (c0 + u * 32) * 8, plane, planes, v[u]);
+      }
     }
   }
-  for (int c0 = lane * 8; c0 < d; c0 += 512) {
-    float v[2][8];
+  if constexpr (sizeof(T) == 2) {
+    for (int c0 = done + lane * 8; c0 < d; c0 += 512) {
+      __align__(16) bf16 v[2][8];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) row8(x, c0 + u * 256, d, vec, v[u]);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      if (c0 + u * 256 < d) planes8(out + c0 + u * 256, plane, planes, v[u]);
+        for (int j = 0; j < 8; ++j) {
+          const int c = c0 + u * 256 + j;
+          v[u][j] = c < d ? x[c] : from_f32<bf16>(0.f);
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)  // up to seven zeros behind the row, inside its pitch
+        if (c0 + u * 256 < d) *reinterpret_cast<uint4*>(out + c0 + u * 256) = *reinterpret_cast<const uint4*>(v[u]);
+    }
+    return;
+  }
+  for (int c0 = done + lane; c0 < d; c0 += 256) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = c0 + u * 32 < d ? to_f32(x[c0 + u * 32]) : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (c0 + u * 32 >= d) continue;
+      for (int p = 0; p < planes; ++p) {
+        const bf16 h = from_f32<bf16>(v[u]);
+        out[p * plane + c0 + u * 32] = h;
+        v[u] -= to_f32(h);
+      }
+    }
   }
 }
 // One row as two fp16 planes of x * 2^e; returns 2^-e.
 __device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __half* out, int64_t plane) {
   const int lane = threadIdx.x & 31;
+  const int d8 = vec ? d / 8 : 0;  // groups of eight; what is left goes lane by lane
   float m = 0.f;
-  for (int c0 = lane * 8; c0 < d; c0 += 512) {
-    float v[2][8];
+  for (int c0 = lane; c0 < d8; c0 += 64) {
+    float v[2][8] = {};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) row8(x, c0 + u * 256, d, vec, v[u]);
+    for (int u = 0; u < 2; ++u)
+      if (c0 + u * 32 < d8) load8(x + (c0 + u * 32) * 8, v[u]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(v[0][j]), fabsf(v[1][j])));
+  }
+  for (int c0 = d8 * 8 + lane; c0 < d; c0 += 256) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = c0 + u * 32 < d ? x[c0 + u * 32] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(v[u]));
   }
   m = warp_max(m);
   // exponent of the largest element; 2^e within the normal numbers
   const int top = (int)(__float_as_uint(m) >> 23) - 127;
   const int e = max(-112, min(126, 14 - top));
   const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-  for (int c0 = lane * 8; c0 < d; c0 += 512) {
-    float v[2][8];
+  for (int c0 = lane; c0 < d8; c0 += 32) {
+    float v[8];
+    load8(x + c0 * 8, v);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) row8(x, c0 + u * 256, d, vec, v[u]);
+    for (int p = 0; p < 2; ++p) {
+      __half2 h[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (c0 + u * 256 >= d) continue;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        __half2 h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float &a = v[u][2 * j], &b = v[u][2 * j + 1];
-          if (p == 0) {
-            a *= up;
-            b *= up;
-          }
-          h[j] = __floats2half2_rn(a, b);
-          a -= __low2float(h[j]);
-          b -= __high2float(h[j]);
+      for (int j = 0; j < 4; ++j) {
+        float &a = v[2 * j], &b = v[2 * j + 1];
+        if (p == 0) {
+          a *= up;
+          b *= up;
         }
-        *reinterpret_cast<uint4*>(out + p * plane + c0 + u * 256) = *reinterpret_cast<const uint4*>(h);
+        h[j] = __floats2half2_rn(a, b);
+        a -= __low2float(h[j]);
+        b -= __high2float(h[j]);
       }
+      *reinterpret_cast<uint4*>(out + p * plane + c0 * 8) = *reinterpret_cast<const uint4*>(h);
+    }
+  }
+  for (int c0 = d8 * 8 + lane; c0 < d; c0 += 256) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = c0 + u * 32 < d ? x[c0 + u * 32] * up : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (c0 + u * 32 >= d) continue;
+      const __half h = __float2half_rn(v[u]);
+      out[c0 + u * 32] = h;
+      out[plane + c0 + u * 32] = __float2half_rn(v[u] - __half2float(h));
     }
   }
   return __uint_as_float((uint32_t)(127 - e) << 23);
