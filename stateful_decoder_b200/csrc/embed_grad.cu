@@ -152,15 +152,14 @@ __device__ __forceinline__ void scan_hist(uint32_t (*hist)[256], uint32_t* total
 struct ZeroRows {
   uint8_t* p;
   int64_t row_bytes, ld_bytes;  // multiples of the element size
-  int V, vec, elem;             // vec: 16-byte stores
+  int V, elem, whole;           // whole: no gaps between rows, base 16-byte aligned
   int part, parts;
 };
 __device__ __forceinline__ void zero_rows(const ZeroRows& z, int b, int blocks, int threads) {
-  const int64_t unit = z.vec ? 16 : z.elem;
-  const int64_t per_row = z.row_bytes / unit;
-  const int64_t n = per_row * z.V, step = (int64_t)blocks * threads, end = n * (z.part + 1) / z.parts;
-  int64_t i = n * z.part / z.parts + (int64_t)b * threads + threadIdx.x;
-  if (z.vec && z.row_bytes == z.ld_bytes) {
+  const int64_t step = (int64_t)blocks * threads, at = (int64_t)b * threads + threadIdx.x;
+  if (z.whole) {  // one stretch of memory: 16 bytes at a time, whatever its rows are
+    const int64_t bytes = z.row_bytes * z.V, n = bytes / 16, end = n * (z.part + 1) / z.parts;
+    int64_t i = n * z.part / z.parts + at;
     uint4* p = reinterpret_cast<uint4*>(z.p);
     const uint4 zero = make_uint4(0, 0, 0, 0);
     for (; i + 3 * step < end; i += 4 * step) {
@@ -170,12 +169,13 @@ __device__ __forceinline__ void zero_rows(const ZeroRows& z, int b, int blocks, 
       p[i + 3 * step] = zero;
     }
     for (; i < end; i += step) p[i] = zero;
+    if (z.part + 1 == z.parts && at < bytes % 16) z.p[n * 16 + at] = 0;
     return;
   }
-  for (; i < end; i += step) {
-    uint8_t* p = z.p + i / per_row * z.ld_bytes + i % per_row * unit;
-    if (z.vec) *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-    else if (z.elem == 4) *reinterpret_cast<uint32_t*>(p) = 0;
+  const int64_t per_row = z.row_bytes / z.elem, n = per_row * z.V, end = n * (z.part + 1) / z.parts;
+  for (int64_t i = n * z.part / z.parts + at; i < end; i += step) {
+    uint8_t* p = z.p + i / per_row * z.ld_bytes + i % per_row * z.elem;
+    if (z.elem == 4) *reinterpret_cast<uint32_t*>(p) = 0;
     else *reinterpret_cast<uint16_t*>(p) = 0;
   }
 }
@@ -552,7 +552,7 @@ cudaError_t gradient(const void* dout_, int64_t ld_dout, const int32_t* tok, int
     z.row_bytes = (int64_t)d * z.elem;
     z.ld_bytes = ld_demb * z.elem;
     z.V = V;
-    z.vec = aligned16(demb, ld_demb) && z.row_bytes % 16 == 0;
+    z.whole = ld_demb == d && (reinterpret_cast<uintptr_t>(demb) & 15) == 0;
   }
   const unsigned idle = accumulate ? 0 : (unsigned)std::min<int64_t>(
       kSmCount, ((int64_t)V * d + 16383) / 16384);  // zeroing blocks, 16k elements each or more
