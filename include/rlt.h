@@ -488,7 +488,7 @@ int32_t rlt_op_cross_entropy(const rlt_vocab* a, const int32_t* target_dev, floa
  * dh = dz w, dw = dz^T h.  dh_dev [N][d] (rows ld_dh apart) is written whole
  * (zeros for rows without a target or of weight 0, whose h is not used);
  * dw_dev [V][d] is written whole or, with accumulate_dw, added to.  Either
- * may be NULL, not both; neither may overlap an operand.  Sums are fp32; with
+ * may be NULL, not both; neither may overlap an operand or the other.  Sums are fp32; with
  * bf16 operands dz is rounded to bf16 once, as an operand of the two products
  * (to 16 bits for up to 256 rows).  The workspace holds up to 512 MB of dz, or
  * 2048 columns of it where that is more.

@@ -1890,7 +1890,7 @@ int32_t vocab_problem(const rlt_vocab* a, const int32_t* ids, const float* teach
 }
 
 int32_t vocab_forward_call(const VocabLoss& p, float* loss, float* lse, void* ws, size_t* ws_bytes, void* stream) {
-  if (p.N > 0 && (!loss || !lse)) return fail(RLT_E_INVAL, "null output");
+  if (p.N > 0 && (!loss || !lse || loss == lse)) return fail(RLT_E_INVAL, "null output, or one for two");
   bool report;
   RLT_TRY(check_workspace(ws, ws_bytes, vocab_workspace_bytes(p, 0), &report));
   if (!report) RLT_CUDA(vocab_forward(p, loss, lse, ws, (cudaStream_t)stream));
@@ -1903,6 +1903,8 @@ int32_t vocab_backward_call(const VocabLoss& p, const float* lse, const float* w
   if (p.N > 0 && (!lse || !weight)) return fail(RLT_E_INVAL, "null lse or weight");
   if (!dh && !dw) return fail(RLT_E_INVAL, "no gradient requested");
   if ((dh && ld_dh < p.d) || (dw && ld_dw < p.d)) return fail(RLT_E_INVAL, "gradient rows need ld >= d");
+  if (p.N > 0 && (dh == p.h || dh == p.w || dw == p.h || dw == p.w || dh == dw))
+    return fail(RLT_E_INVAL, "a gradient may not take an operand's place, nor the other's");
   bool report;
   RLT_TRY(check_workspace(ws, ws_bytes, vocab_workspace_bytes(p, 1), &report));
   if (!report)
@@ -1957,6 +1959,7 @@ int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int
   if (!extents(N, V, d) || ld_emb < d || ld_out < d || !emb_dev || (N > 0 && (!tok_dev || !out_dev)))
     return fail(RLT_E_INVAL, "bad embedding arguments");
   if (!known_dtype(emb_dtype) || !known_dtype(out_dtype)) return fail(RLT_E_INVAL, "dtype");
+  if (N > 0 && out_dev == emb_dev) return fail(RLT_E_INVAL, "the output may not take the table's place");
   RLT_CUDA(embed_lookup(emb_dev, ld_emb, emb_dtype, V, d, tok_dev, N, scale, out_dev, ld_out, out_dtype,
                         (cudaStream_t)stream));
   return ok();
@@ -1969,6 +1972,7 @@ int32_t rlt_op_embed_backward(const void* dout_dev, int64_t ld_dout, int32_t dou
       (N > 0 && (!tok_dev || !dout_dev)))
     return fail(RLT_E_INVAL, "bad embedding gradient arguments");
   if (!known_dtype(dout_dtype) || !known_dtype(demb_dtype)) return fail(RLT_E_INVAL, "dtype");
+  if (N > 0 && dout_dev == demb_dev) return fail(RLT_E_INVAL, "the gradient may not take dout's place");
   bool report;
   RLT_TRY(check_workspace(ws_dev, ws_bytes, embed_backward_workspace_bytes(N, V, d), &report));
   if (!report)

@@ -12,7 +12,8 @@ def rlt():
     return rlt
 
 
-P = ctypes.c_void_p(4096)  # a pointer that no refused call follows
+P = ctypes.c_void_p(4096)  # pointers that no refused call follows
+Q, R = ctypes.c_void_p(8192), ctypes.c_void_p(12288)
 
 
 def operands(rlt, **kw):
@@ -54,6 +55,20 @@ def test_operands_are_checked(rlt):
     assert back(a, P, P, P, P, 64, P, 63, 0, P, sized(BIG), None) == rlt.RLT_E_INVAL
 
 
+def test_outputs_in_an_operands_place_are_refused(rlt):
+    """By their addresses: an output that is an operand, or the other output."""
+    lib = rlt._lib
+    a = ctypes.byref(operands(rlt, h=4096, w=8192))
+    assert lib.rlt_op_cross_entropy(a, P, R, R, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert lib.rlt_op_distill(a, P, P, 4, 1.0, R, R, P, sized(BIG), None) == rlt.RLT_E_INVAL
+    other = ctypes.c_void_p(1 << 20)
+    for dh, dw in ((P, R), (Q, R), (R, P), (R, Q), (R, R), (P, None), (None, Q)):
+        assert lib.rlt_op_cross_entropy_backward(a, other, other, other, dh, 64, dw, 64, 0, other, sized(BIG), None) == rlt.RLT_E_INVAL
+        assert lib.rlt_op_distill_backward(a, other, other, 4, 1.0, other, other, dh, 64, dw, 64, 0, other, sized(BIG), None) == rlt.RLT_E_INVAL
+    assert lib.rlt_op_embed(P, 64, 1, 100, 64, Q, 3, 1.0, P, 64, 1, None) == rlt.RLT_E_INVAL
+    assert lib.rlt_op_embed_backward(P, 64, 1, Q, 3, 100, 64, 1.0, P, 64, 1, 0, R, sized(BIG), None) == rlt.RLT_E_INVAL
+
+
 def test_embedding_arguments_are_checked(rlt):
     lib = rlt._lib
     good = [P, 64, 1, 100, 64, P, 3, 1.0, P, 64, 0, None]
@@ -74,10 +89,10 @@ def test_workspace_convention(rlt):
     a = ctypes.byref(operands(rlt, N=300, V=5000))
     n = ctypes.c_size_t()
     calls = (
-        lambda ws, s: lib.rlt_op_cross_entropy(a, P, P, P, ws, s, None),
-        lambda ws, s: lib.rlt_op_cross_entropy_backward(a, P, P, P, P, 64, P, 64, 0, ws, s, None),
-        lambda ws, s: lib.rlt_op_distill(a, P, P, 50, 0.8, P, P, ws, s, None),
-        lambda ws, s: lib.rlt_op_distill_backward(a, P, P, 50, 0.8, P, P, P, 64, P, 64, 0, ws, s, None),
+        lambda ws, s: lib.rlt_op_cross_entropy(a, P, P, Q, ws, s, None),
+        lambda ws, s: lib.rlt_op_cross_entropy_backward(a, P, P, P, Q, 64, R, 64, 0, ws, s, None),
+        lambda ws, s: lib.rlt_op_distill(a, P, P, 50, 0.8, P, Q, ws, s, None),
+        lambda ws, s: lib.rlt_op_distill_backward(a, P, P, 50, 0.8, P, P, Q, 64, R, 64, 0, ws, s, None),
     )
     for call in calls:
         assert call(None, ctypes.byref(n)) == rlt.RLT_OK
@@ -94,9 +109,9 @@ def test_workspace_does_not_hold_the_logits(rlt):
     lib = rlt._lib
     n = ctypes.c_size_t()
     a = ctypes.byref(operands(rlt, N=65536, V=256000, d=2048, ld_h=2048, ld_w=2048))
-    assert lib.rlt_op_cross_entropy(a, P, P, P, None, ctypes.byref(n), None) == rlt.RLT_OK
+    assert lib.rlt_op_cross_entropy(a, P, P, Q, None, ctypes.byref(n), None) == rlt.RLT_OK
     assert n.value < 2 << 30
-    assert lib.rlt_op_cross_entropy_backward(a, P, P, P, P, 2048, P, 2048, 0, None, ctypes.byref(n), None) == rlt.RLT_OK
+    assert lib.rlt_op_cross_entropy_backward(a, P, P, P, Q, 2048, R, 2048, 0, None, ctypes.byref(n), None) == rlt.RLT_OK
     assert n.value < 4 << 30
 
 
