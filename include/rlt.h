@@ -449,7 +449,8 @@ int32_t rlt_op_sample(const float* logits_dev, int32_t B, int32_t V, const rlt_s
 
 /* Operands of the loss over the vocabulary: N rows of h (a readout operand,
  * report eq. 2.6) against the V rows of w (a readout or embedding matrix),
- * both row-major in `dtype` with rows ld_* elements apart (ld >= d), finite.
+ * both row-major in `dtype` with rows ld_* elements apart (ld >= d), finite
+ * (fp32: below 2^127 in magnitude).
  * Any N >= 0, V >= 1, d >= 1 up to 2^28 and any row distance; bf16 operands
  * whose base is not 16-byte aligned or whose ld % 8 != 0 are copied into the
  * workspace first.  The logits are
@@ -522,7 +523,8 @@ int32_t rlt_op_distill_backward(const rlt_vocab* a, const int32_t* ids_dev, cons
 /* Embedding lookup (the model's first step, with a scale):
  * out[n][:] = scale * emb[tok[n]][:] for n < N, emb [V][d] in emb_dtype, out
  * [N][d] in out_dtype, rows ld_* elements apart; the product is fp32 and
- * rounded once.  An id outside [0, V) gives a zero row.  Errors: RLT_E_INVAL, RLT_E_CUDA. */
+ * rounded once.  An id outside [0, V) gives a zero row.  Extents up to 2^28.
+ * Errors: RLT_E_INVAL, RLT_E_CUDA. */
 int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int32_t V, int32_t d,
                      const int32_t* tok_dev, int32_t N, float scale, void* out_dev, int64_t ld_out,
                      int32_t out_dtype, void* stream);
@@ -532,6 +534,7 @@ int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int
  * that do not occur).  The ids are sorted and every row is summed in fp32 in an
  * order that depends on N, d and the ids alone.  dout [N][d] in dout_dtype,
  * demb [V][d] in demb_dtype.  Ids outside [0, V) contribute nothing and their dout is not read.
+ * N and V up to 2^28, d up to 2^23.
  * Errors: RLT_E_INVAL, RLT_E_CAPACITY (workspace too small), RLT_E_CUDA. */
 int32_t rlt_op_embed_backward(const void* dout_dev, int64_t ld_dout, int32_t dout_dtype, const int32_t* tok_dev,
                               int32_t N, int32_t V, int32_t d, float scale, void* demb_dev, int64_t ld_demb,

@@ -1857,6 +1857,7 @@ bool known_dtype(int32_t t) { return t == RLT_DTYPE_F32 || t == RLT_DTYPE_BF16; 
 
 // Extents the kernels' 32-bit row and column numbers hold with room to spare.
 constexpr int32_t kMaxExtent = 1 << 28;
+constexpr int32_t kMaxSummed = 1 << 23;  // of the embedding gradient's d: a grid's second extent ends at 65,535 blocks
 bool extents(int32_t N, int32_t V, int32_t d) {
   return N >= 0 && V >= 1 && d >= 1 && N <= kMaxExtent && V <= kMaxExtent && d <= kMaxExtent;
 }
@@ -1968,7 +1969,7 @@ int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int
 int32_t rlt_op_embed_backward(const void* dout_dev, int64_t ld_dout, int32_t dout_dtype, const int32_t* tok_dev,
                               int32_t N, int32_t V, int32_t d, float scale, void* demb_dev, int64_t ld_demb,
                               int32_t demb_dtype, int32_t accumulate, void* ws_dev, size_t* ws_bytes, void* stream) {
-  if (!extents(N, V, d) || ld_dout < d || ld_demb < d || !demb_dev || !ws_bytes ||
+  if (!extents(N, V, d) || d > kMaxSummed || ld_dout < d || ld_demb < d || !demb_dev || !ws_bytes ||
       (N > 0 && (!tok_dev || !dout_dev)))
     return fail(RLT_E_INVAL, "bad embedding gradient arguments");
   if (!known_dtype(dout_dtype) || !known_dtype(demb_dtype)) return fail(RLT_E_INVAL, "dtype");

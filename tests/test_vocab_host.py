@@ -71,16 +71,19 @@ def test_outputs_in_an_operands_place_are_refused(rlt):
 
 def test_embedding_arguments_are_checked(rlt):
     lib = rlt._lib
-    good = [P, 64, 1, 100, 64, P, 3, 1.0, P, 64, 0, None]
+    good = [P, 64, 1, 100, 64, P, 3, 1.0, Q, 64, 0, None]
     for at, bad in ((0, None), (1, 63), (2, 2), (3, 0), (4, 0), (5, None), (6, -1), (8, None), (9, 63), (10, -1)):
         args = list(good)
         args[at] = bad
         assert lib.rlt_op_embed(*args) == rlt.RLT_E_INVAL, at
-    good = [P, 64, 1, P, 3, 100, 64, 1.0, P, 64, 0, 0, P, sized(BIG), None]
+    good = [P, 64, 1, P, 3, 100, 64, 1.0, Q, 64, 0, 0, R, sized(BIG), None]
     for at, bad in ((0, None), (1, 63), (2, 7), (3, None), (4, -1), (5, 0), (6, 0), (8, None), (9, 63), (10, 2), (13, None)):
         args = list(good)
         args[at] = bad
         assert lib.rlt_op_embed_backward(*args) == rlt.RLT_E_INVAL, at
+    size, wide = ctypes.c_size_t(), 1 << 23
+    for d, code in ((wide, rlt.RLT_OK), (wide + 1, rlt.RLT_E_INVAL)):
+        assert lib.rlt_op_embed_backward(P, d, 1, P, 3, 100, d, 1.0, Q, d, 0, 0, None, ctypes.byref(size), None) == code
 
 
 def test_workspace_convention(rlt):
