@@ -468,7 +468,8 @@ typedef struct rlt_vocab {
 } rlt_vocab;
 
 /* Workspace of the calls below: with ws_dev == NULL nothing is launched and
- * *ws_bytes receives the bytes the call needs; otherwise *ws_bytes is the size
+ * *ws_bytes receives the bytes the call needs (256 at least, also where there
+ * are no rows); otherwise *ws_bytes is the size
  * of ws_dev (256-byte aligned device memory, contents arbitrary).  The memory
  * belongs to the call until its work on `stream` is done: calls that may
  * overlap on the GPU, replays of captured graphs among them, need their own.

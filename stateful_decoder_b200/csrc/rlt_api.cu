@@ -1862,8 +1862,11 @@ bool extents(int32_t N, int32_t V, int32_t d) {
   return N >= 0 && V >= 1 && d >= 1 && N <= kMaxExtent && V <= kMaxExtent && d <= kMaxExtent;
 }
 
-// The workspace convention: reports the size (returns 1 with ws null), or checks it.
+// The workspace convention: reports the size (*report: ws is null), or checks
+// it.  A reported size is never 0: a caller's allocation of 0 bytes may be the
+// null pointer, and the call that follows would then ask again and do nothing.
 int32_t check_workspace(void* ws, size_t* ws_bytes, size_t need, bool* report) {
+  need = std::max<size_t>(need, 256);
   *report = ws == nullptr;
   if (*report) {
     *ws_bytes = need;

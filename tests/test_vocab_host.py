@@ -118,6 +118,27 @@ def test_workspace_does_not_hold_the_logits(rlt):
     assert n.value < 4 << 30
 
 
+@pytest.mark.parametrize("N", [0, 1])
+def test_a_reported_size_is_never_zero(rlt, N):
+    """With no rows too: an allocation of 0 bytes may be the null pointer, which
+    asks for the size again and launches nothing, so a gradient that is to be
+    written whole (zeros) would keep what it held."""
+    lib = rlt._lib
+    a = ctypes.byref(operands(rlt, N=N))
+    n = ctypes.c_size_t(0)
+    for call in (
+        lambda ws, s: lib.rlt_op_cross_entropy(a, P, P, Q, ws, s, None),
+        lambda ws, s: lib.rlt_op_cross_entropy_backward(a, P, P, P, Q, 64, R, 64, 0, ws, s, None),
+        lambda ws, s: lib.rlt_op_distill(a, P, P, 4, 0.8, P, Q, ws, s, None),
+        lambda ws, s: lib.rlt_op_distill_backward(a, P, P, 4, 0.8, P, P, Q, 64, R, 64, 0, ws, s, None),
+        lambda ws, s: lib.rlt_op_embed_backward(P, 64, 1, P, N, 100, 64, 1.0, Q, 64, 0, 0, ws, s, None),
+    ):
+        n.value = 0
+        assert call(None, ctypes.byref(n)) == rlt.RLT_OK
+        assert n.value >= 256
+        assert call(R, sized(0)) == rlt.RLT_E_CAPACITY
+
+
 class _Fake:
     """A CPU tensor that passes for a CUDA one: what the binding refuses, it
     refuses by shape, type and stride, before the library sees a pointer."""
