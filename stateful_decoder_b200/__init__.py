@@ -513,6 +513,8 @@ def _with_workspace(fn, args, like, workspace, stream) -> None:
     """fn(*args, ws, size*, stream) with the caller's workspace (a uint8 CUDA
     tensor) or one of the size the call asks for, from torch's allocator on
     the stream the call runs on."""
+    if workspace is not None and workspace.numel() == 0:
+        raise ValueError("workspace: empty (the library would take its null pointer for a question of the size)")
     st = _stream(stream)
     size = ctypes.c_size_t()
     if workspace is None:

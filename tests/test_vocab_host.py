@@ -191,3 +191,26 @@ def test_binding_refuses_wrong_tensors(rlt, monkeypatch):
     far.device = types.SimpleNamespace(index=1)
     with pytest.raises(ValueError, match="current device"):
         rlt.rlt_op_cross_entropy(h, far, t, o, e)
+
+
+def test_binding_refuses_an_empty_workspace(rlt, monkeypatch):
+    """A tensor without elements has a null pointer, which asks the library for
+    the size: the call would return with nothing launched."""
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    def f(*shape, dtype=torch.float32):
+        return _Fake(torch.zeros(*shape, dtype=dtype))
+
+    i32 = torch.int32
+    h, w, t, o, e = f(4, 8), f(9, 8), f(4, dtype=i32), f(4), f(4)
+    ids, te, none = f(4, 3, dtype=i32), f(4, 3), f(0, dtype=torch.uint8)
+    for call in (
+        lambda: rlt.rlt_op_cross_entropy(h, w, t, o, e, workspace=none, stream=0),
+        lambda: rlt.rlt_op_cross_entropy_backward(h, w, t, e, o, dh=f(4, 8), workspace=none, stream=0),
+        lambda: rlt.rlt_op_distill(h, w, ids, te, 1.0, o, e, workspace=none, stream=0),
+        lambda: rlt.rlt_op_distill_backward(h, w, ids, te, 1.0, e, o, dw=f(9, 8), workspace=none, stream=0),
+        lambda: rlt.rlt_op_embed_backward(f(4, 8), t, w, workspace=none, stream=0),
+    ):
+        with pytest.raises(ValueError, match="workspace"):
+            call()
