@@ -474,7 +474,10 @@ typedef struct rlt_vocab {
  * belongs to the call until its work on `stream` is done: calls that may
  * overlap on the GPU, replays of captured graphs among them, need their own.
  * The calls allocate nothing, wait for nothing on the host, and can be
- * captured into a graph.  Results do not depend on timing. */
+ * captured into a graph.  Results do not depend on timing.
+ * No output may share memory with an operand, the workspace or another output
+ * (RLT_E_INVAL); slices of one buffer that lie between each other's rows do
+ * not. */
 
 /* Softmax cross entropy over the vocabulary, as rlt_replay_backward's loss:
  *   lse[n] = log sum_v exp z[n][v],  logp[n] = z[n][target[n]] - lse[n].
@@ -490,8 +493,7 @@ int32_t rlt_op_cross_entropy(const rlt_vocab* a, const int32_t* target_dev, floa
  * dh = dz w, dw = dz^T h.  dh_dev [N][d] (rows ld_dh apart) is written whole
  * (zeros for rows without a target or of weight 0, whose h is not used);
  * dw_dev [V][d] is written whole or, with accumulate_dw, added to.  Either
- * may be NULL, not both; neither may overlap an operand or the other.  Sums are fp32; with
- * bf16 operands dz is rounded to bf16 once, as an operand of the two products
+ * may be NULL, not both.  Sums are fp32; with bf16 operands dz is rounded to bf16 once, as an operand of the two products
  * (to 16 bits for up to 256 rows).  The workspace holds up to 512 MB of dz, or
  * 2048 columns of it where that is more.
  * Errors: as rlt_op_cross_entropy. */

@@ -23,6 +23,7 @@
 #include <type_traits>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <set>
@@ -1879,6 +1880,54 @@ int32_t check_workspace(void* ws, size_t* ws_bytes, size_t need, bool* report) {
   return RLT_OK;
 }
 
+// A matrix in memory, by its bytes (a vector: one row).
+struct Region {
+  const void* p;
+  int64_t rows, row_bytes, pitch;
+};
+Region vector_region(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+// Do two matrices share a byte?  Slices of one buffer that lie side by side
+// between each other's rows do not.
+bool share_bytes(Region a, Region b) {
+  using wide = __int128;  // row distances are the caller's: extents may pass 64 bits
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.row_bytes <= 0 || b.row_bytes <= 0) return false;
+  for (Region* r : {&a, &b})  // without gaps: one row
+    if (r->pitch == r->row_bytes) *r = vector_region(r->p, r->rows * r->row_bytes);
+  if (a.rows > b.rows) std::swap(a, b);
+  const wide a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p), D = b0 - a0;
+  const wide a_size = (wide)(a.rows - 1) * a.pitch + a.row_bytes, b_size = (wide)(b.rows - 1) * b.pitch + b.row_bytes;
+  if (D >= a_size || -D >= b_size) return false;
+  if (a.rows > 1 && a.pitch == b.pitch) {
+    // Rows i and j meet if -b.row_bytes < D + k pitch < a.row_bytes for k = j -
+    // i, which lies in (-a.rows, b.rows): only the two k about -D / pitch can.
+    const wide q = -D / a.pitch;
+    for (wide k = q - 1; k <= q + 1; ++k)
+      if (k > -a.rows && k < b.rows && D + k * a.pitch < a.row_bytes && D + k * a.pitch > -b.row_bytes) return true;
+    return false;
+  }
+  for (int64_t i = 0; i < a.rows; ++i) {
+    // the first row of b that ends behind the beginning of a's row i
+    const wide s = (wide)i * a.pitch - D, first = s < b.row_bytes ? 0 : (s - b.row_bytes) / b.pitch + 1;
+    if (first < b.rows && first * b.pitch < s + a.row_bytes) return true;
+  }
+  return false;
+}
+// No output may share memory with another, with an operand or with the workspace.
+int32_t check_overlap(std::initializer_list<Region> outputs, std::initializer_list<Region> others) {
+  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Region& r : others)
+      if (share_bytes(*o, r)) return fail(RLT_E_INVAL, "an output overlaps an operand or the workspace");
+    for (auto r = o + 1; r != outputs.end(); ++r)
+      if (share_bytes(*o, *r)) return fail(RLT_E_INVAL, "an output overlaps another");
+  }
+  return RLT_OK;
+}
+int64_t dtype_bytes(int32_t t) { return t == RLT_DTYPE_BF16 ? 2 : 4; }
+Region matrix_region(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+  const int64_t e = dtype_bytes(dtype);
+  return {p, rows, cols * e, rows > 1 ? (ld > INT64_MAX / e ? INT64_MAX : ld * e) : cols * e};
+}
+
 int32_t vocab_problem(const rlt_vocab* a, const int32_t* ids, const float* teacher, int32_t K, float temperature,
                       const size_t* ws_bytes, VocabLoss* p) {
   if (!a || !ws_bytes) return fail(RLT_E_INVAL, "null operands or workspace size");
@@ -1896,8 +1945,14 @@ int32_t vocab_problem(const rlt_vocab* a, const int32_t* ids, const float* teach
 int32_t vocab_forward_call(const VocabLoss& p, float* loss, float* lse, void* ws, size_t* ws_bytes, void* stream) {
   if (p.N > 0 && (!loss || !lse || loss == lse)) return fail(RLT_E_INVAL, "null output, or one for two");
   bool report;
-  RLT_TRY(check_workspace(ws, ws_bytes, vocab_workspace_bytes(p, 0), &report));
-  if (!report) RLT_CUDA(vocab_forward(p, loss, lse, ws, (cudaStream_t)stream));
+  const size_t need = vocab_workspace_bytes(p, 0);
+  RLT_TRY(check_workspace(ws, ws_bytes, need, &report));
+  if (report) return ok();
+  const int64_t n = p.N, list = n * p.K * 4;
+  RLT_TRY(check_overlap({vector_region(loss, n * 4), vector_region(lse, n * 4)},
+                        {matrix_region(p.h, n, p.d, p.ld_h, p.dtype), matrix_region(p.w, p.V, p.d, p.ld_w, p.dtype),
+                         vector_region(p.ids, list), vector_region(p.teacher, list), vector_region(ws, need)}));
+  RLT_CUDA(vocab_forward(p, loss, lse, ws, (cudaStream_t)stream));
   return ok();
 }
 
@@ -1910,9 +1965,15 @@ int32_t vocab_backward_call(const VocabLoss& p, const float* lse, const float* w
   if (p.N > 0 && (dh == p.h || dh == p.w || dw == p.h || dw == p.w || dh == dw))
     return fail(RLT_E_INVAL, "a gradient may not take an operand's place, nor the other's");
   bool report;
-  RLT_TRY(check_workspace(ws, ws_bytes, vocab_workspace_bytes(p, 1), &report));
-  if (!report)
-    RLT_CUDA(vocab_backward(p, lse, weight, dh, ld_dh, dw, ld_dw, accumulate_dw != 0, ws, (cudaStream_t)stream));
+  const size_t need = vocab_workspace_bytes(p, 1);
+  RLT_TRY(check_workspace(ws, ws_bytes, need, &report));
+  if (report) return ok();
+  const int64_t n = p.N, list = n * p.K * 4;
+  RLT_TRY(check_overlap({matrix_region(dh, n, p.d, ld_dh, p.dtype), matrix_region(dw, p.V, p.d, ld_dw, p.dtype)},
+                        {matrix_region(p.h, n, p.d, p.ld_h, p.dtype), matrix_region(p.w, p.V, p.d, p.ld_w, p.dtype),
+                         vector_region(p.ids, list), vector_region(p.teacher, list), vector_region(lse, n * 4),
+                         vector_region(weight, n * 4), vector_region(ws, need)}));
+  RLT_CUDA(vocab_backward(p, lse, weight, dh, ld_dh, dw, ld_dw, accumulate_dw != 0, ws, (cudaStream_t)stream));
   return ok();
 }
 
@@ -1963,7 +2024,8 @@ int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int
   if (!extents(N, V, d) || ld_emb < d || ld_out < d || !emb_dev || (N > 0 && (!tok_dev || !out_dev)))
     return fail(RLT_E_INVAL, "bad embedding arguments");
   if (!known_dtype(emb_dtype) || !known_dtype(out_dtype)) return fail(RLT_E_INVAL, "dtype");
-  if (N > 0 && out_dev == emb_dev) return fail(RLT_E_INVAL, "the output may not take the table's place");
+  RLT_TRY(check_overlap({matrix_region(out_dev, N, d, ld_out, out_dtype)},
+                        {matrix_region(emb_dev, V, d, ld_emb, emb_dtype), vector_region(tok_dev, (int64_t)N * 4)}));
   RLT_CUDA(embed_lookup(emb_dev, ld_emb, emb_dtype, V, d, tok_dev, N, scale, out_dev, ld_out, out_dtype,
                         (cudaStream_t)stream));
   return ok();
@@ -1978,10 +2040,14 @@ int32_t rlt_op_embed_backward(const void* dout_dev, int64_t ld_dout, int32_t dou
   if (!known_dtype(dout_dtype) || !known_dtype(demb_dtype)) return fail(RLT_E_INVAL, "dtype");
   if (N > 0 && dout_dev == demb_dev) return fail(RLT_E_INVAL, "the gradient may not take dout's place");
   bool report;
-  RLT_TRY(check_workspace(ws_dev, ws_bytes, embed_backward_workspace_bytes(N, V, d), &report));
-  if (!report)
-    RLT_CUDA(embed_backward(dout_dev, ld_dout, dout_dtype, tok_dev, N, V, d, scale, demb_dev, ld_demb, demb_dtype,
-                            accumulate != 0, ws_dev, (cudaStream_t)stream));
+  const size_t need = embed_backward_workspace_bytes(N, V, d);
+  RLT_TRY(check_workspace(ws_dev, ws_bytes, need, &report));
+  if (report) return ok();
+  RLT_TRY(check_overlap({matrix_region(demb_dev, V, d, ld_demb, demb_dtype)},
+                        {matrix_region(dout_dev, N, d, ld_dout, dout_dtype), vector_region(tok_dev, (int64_t)N * 4),
+                         vector_region(ws_dev, need)}));
+  RLT_CUDA(embed_backward(dout_dev, ld_dout, dout_dtype, tok_dev, N, V, d, scale, demb_dev, ld_demb, demb_dtype,
+                          accumulate != 0, ws_dev, (cudaStream_t)stream));
   return ok();
 }
 

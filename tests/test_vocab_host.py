@@ -118,6 +118,55 @@ def test_workspace_does_not_hold_the_logits(rlt):
     assert n.value < 4 << 30
 
 
+def test_outputs_that_reach_into_an_operand_are_refused(rlt):
+    """By their whole extents, not their first addresses: an output that begins
+    inside an operand or ends in it, in the workspace, or in the other output.
+    (Every call here is refused: the addresses are not memory.)"""
+    lib = rlt._lib
+    MB = 1 << 20
+
+    def at(n, off=0):
+        return ctypes.c_void_p(n * MB + off)
+
+    H, W, IDS, TE, O1, O2, WS = 16, 32, 48, 49, 50, 51, 64
+    N, V, d = 3, 100, 64  # bf16: rows of 128 bytes, h 384 bytes, w 12,800
+    a = ctypes.byref(operands(rlt, h=H * MB, w=W * MB, N=N, V=V, d=d))
+    for o in (at(H, 4), at(H, -4), at(H, 380), at(W, 12796), at(IDS, -8), at(IDS, 8), at(O2, 8), at(O2, -8), at(WS, 4)):
+        assert lib.rlt_op_cross_entropy(a, at(IDS), o, at(O2), at(WS), sized(BIG), None) == rlt.RLT_E_INVAL, o
+        assert lib.rlt_op_cross_entropy(a, at(IDS), at(O2), o, at(WS), sized(BIG), None) == rlt.RLT_E_INVAL, o
+    for o in (at(H, 4), at(W, 12796), at(IDS, 44), at(TE, -8), at(TE, 44), at(O2, 8), at(WS, 4)):
+        assert lib.rlt_op_distill(a, at(IDS), at(TE), 4, 1.0, o, at(O2), at(WS), sized(BIG), None) == rlt.RLT_E_INVAL, o
+
+    def back(dh, ld_dh, dw, ld_dw, a=a):
+        return (lib.rlt_op_cross_entropy_backward(a, at(IDS), at(O1), at(O2), dh, ld_dh, dw, ld_dw, 0, at(WS), sized(BIG), None),
+                lib.rlt_op_distill_backward(a, at(IDS), at(TE), 4, 1.0, at(O1), at(O2), dh, ld_dh, dw, ld_dw, 0, at(WS), sized(BIG), None))
+
+    refused = (rlt.RLT_E_INVAL, rlt.RLT_E_INVAL)
+    for g in (at(H, 64), at(H, -64), at(W, 12672), at(W, -256), at(IDS, 8), at(O1, -380), at(O2, 8), at(WS, 128)):
+        assert back(g, d, None, 0) == refused, g
+    for g in (at(H, 64), at(W, 64), at(W, -12672), at(H, -12672), at(IDS, 0), at(O1, 0), at(O2, -12672), at(WS, 0)):
+        assert back(None, 0, g, d) == refused, g
+    assert back(at(80), d, at(80, 256), d) == refused
+    # rows that stand apart: a gradient whose rows reach into the operand's, at
+    # the operand's own row distance and at another
+    a2 = ctypes.byref(operands(rlt, h=H * MB, ld_h=200, w=W * MB, ld_w=200, N=N, V=V, d=d))
+    for off in (126, -126, 400 + 126, -800 - 126, 99 * 400 - 126):
+        assert back(None, 0, at(W, off), 200, a2) == refused, off
+    assert back(None, 0, at(W, 126), 1000, a2) == refused
+    assert back(None, 0, at(W, 3 * 400 + 200), 201, a2) == refused  # meets w's rows further on
+    assert back(at(W, 126), 1000, None, 0, a2) == refused
+    assert back(at(W, 99 * 400 + 126), 1000, None, 0, a2) == refused
+    # no rows: dw is still written whole
+    none = ctypes.byref(operands(rlt, h=None, w=W * MB, N=0, V=V, d=d))
+    assert lib.rlt_op_cross_entropy_backward(none, None, None, None, None, 0, at(W), d, 0, at(WS), sized(BIG), None) == rlt.RLT_E_INVAL
+
+    E, T, G = 16, 32, 48
+    for o in (at(E, 4), at(E, -4), at(T, 8), at(T, -4)):
+        assert lib.rlt_op_embed(at(E), d, 0, V, d, at(T), N, 1.0, o, d, 1, None) == rlt.RLT_E_INVAL, o
+    for o in (at(E, 4), at(E, -4), at(T, 8), at(T, -4), at(WS, 0)):
+        assert lib.rlt_op_embed_backward(at(E), d, 1, at(T), N, V, d, 1.0, o, d, 0, 0, at(WS), sized(BIG), None) == rlt.RLT_E_INVAL, o
+
+
 @pytest.mark.parametrize("N", [0, 1])
 def test_a_reported_size_is_never_zero(rlt, N):
     """With no rows too: an allocation of 0 bytes may be the null pointer, which
