@@ -34,7 +34,9 @@ inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // slots sorted by id (and slot, so the order never depends on timing) in a
 // bitonic network over P >= K keys in shared memory, P / 2 exchanges per stage
 // spread over all lanes; empty slots go last.  some[n] = 0 when no slot
-// carries weight.
+// carries weight.  The maximum is taken off before the division by the
+// temperature: logits at the type's ends (masks of the lowest value) stay
+// finite, so a row of nothing else is uniform, and only -inf is no weight.
 template <int P>
 __global__ void __launch_bounds__(128) teacher_prep_kernel(const int32_t* ids, const float* teacher, int N, int K,
                                                            int V, float inv_t, int32_t* sid, float* sq, float* slogq,
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(128) teacher_prep_kernel(const int32_t* ids, c
 #pragma unroll
   for (int k = lane; k < P; k += 32) {
     const int32_t id = k < K ? ids[n * K + k] : -1;
-    const float t = k < K ? teacher[n * K + k] * inv_t : 0.f;
+    const float t = k < K ? teacher[n * K + k] : 0.f;
     const bool ok = id >= 0 && id < V;
     if (ok) {
       nan |= isnan(t);
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(128) teacher_prep_kernel(const int32_t* ids, c
 #pragma unroll
   for (int k = lane; k < P; k += 32) {
     const unsigned long long key = keys[k];
-    if ((int)(key >> 32) != kNoId) sum += expf(ts[(unsigned)key] - m);
+    if ((int)(key >> 32) != kNoId) sum += expf((ts[(unsigned)key] - m) * inv_t);
   }
   sum = warp_sum(sum);
   const float logsum = logf(sum);
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(128) teacher_prep_kernel(const int32_t* ids, c
     const unsigned long long key = keys[k];
     const int id = (int)(key >> 32);
     const bool on = has && id != kNoId;
-    const float t = on ? ts[(unsigned)key] - m : 0.f;
+    const float t = on ? (ts[(unsigned)key] - m) * inv_t : 0.f;
     sid[n * K + k] = on ? id : kNoId;
     sq[n * K + k] = on ? expf(t) / sum : 0.f;
     slogq[n * K + k] = on ? t - logsum : 0.f;

@@ -35,3 +35,28 @@ def test_gradients_beside_their_operands(env, dtype):
     assert torch.equal(both[V:], w0.float()[tok.long()])
     with pytest.raises(rlt.RltError):
         rlt.rlt_op_embed(both[:V], tok, both[V - 1:V - 1 + N])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [6, 150])
+@pytest.mark.parametrize("T", [0.25, 0.8, 2.0])
+def test_teacher_logits_of_extreme_values(env, T, N, dtype):
+    """Masks of the type's lowest value are a softmax's ordinary members: a row
+    that holds nothing else is uniform, at any temperature; largest values do
+    not overflow; -inf alone empties a row."""
+    rlt, torch = env
+    V, d, K = 300, 32, 8
+    h, w, _, weight = make(torch, N, V, d, dtype, seed=N)
+    ids, teacher = make_list(torch, N, V, K, seed=3, empty=0.0)
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    teacher[0] = low
+    teacher[1, ::2] = low
+    teacher[2] = -math.inf
+    teacher[3], teacher[3, 2:5] = low, high
+    teacher[4], ids[4, 3:] = low, -1
+    teacher[5], teacher[5, 1], teacher[5, 2] = -math.inf, low, low
+    got = kl(env, h, w, ids, teacher, T, weight)
+    ref = reference(torch, h, w, T=T, ids=ids, teacher=teacher, weight=weight)
+    for k in ("loss", "lse", "dh", "dw"):
+        within(torch, got[k], ref[k], k)
+    assert got["loss"][2] == 0 and got["lse"][2] == 0 and got["lse"][0] != 0
