@@ -1928,6 +1928,10 @@ Region matrix_region(const void* p, int64_t rows, int64_t cols, int64_t ld, int3
   return {p, rows, cols * e, rows > 1 ? (ld > INT64_MAX / e ? INT64_MAX : ld * e) : cols * e};
 }
 
+// A single row stands apart from nothing: its distance is whatever the caller
+// has, and strides as long as that fit no tensor map.
+int64_t row_distance(int64_t rows, int32_t d, int64_t ld) { return rows > 1 ? ld : ((int64_t)d + 7) / 8 * 8; }
+
 int32_t vocab_problem(const rlt_vocab* a, const int32_t* ids, const float* teacher, int32_t K, float temperature,
                       const size_t* ws_bytes, VocabLoss* p) {
   if (!a || !ws_bytes) return fail(RLT_E_INVAL, "null operands or workspace size");
@@ -1938,7 +1942,8 @@ int32_t vocab_problem(const rlt_vocab* a, const int32_t* ids, const float* teach
   if (K < 1 || K > 256) return fail(RLT_E_INVAL, "1 <= K <= 256");
   if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
     return fail(RLT_E_INVAL, "temperature > 0");
-  *p = VocabLoss{a->h, a->ld_h, a->w, a->ld_w, a->N, a->V, a->d, a->dtype, ids, teacher, K, 1.f / temperature};
+  *p = VocabLoss{a->h, row_distance(a->N, a->d, a->ld_h), a->w, row_distance(a->V, a->d, a->ld_w), a->N, a->V, a->d,
+                 a->dtype, ids, teacher, K, 1.f / temperature};
   return RLT_OK;
 }
 
@@ -1962,6 +1967,8 @@ int32_t vocab_backward_call(const VocabLoss& p, const float* lse, const float* w
   if (p.N > 0 && (!lse || !weight)) return fail(RLT_E_INVAL, "null lse or weight");
   if (!dh && !dw) return fail(RLT_E_INVAL, "no gradient requested");
   if ((dh && ld_dh < p.d) || (dw && ld_dw < p.d)) return fail(RLT_E_INVAL, "gradient rows need ld >= d");
+  ld_dh = row_distance(p.N, p.d, ld_dh);
+  ld_dw = row_distance(p.V, p.d, ld_dw);
   if (p.N > 0 && (dh == p.h || dh == p.w || dw == p.h || dw == p.w || dh == dw))
     return fail(RLT_E_INVAL, "a gradient may not take an operand's place, nor the other's");
   bool report;
@@ -2026,6 +2033,8 @@ int32_t rlt_op_embed(const void* emb_dev, int64_t ld_emb, int32_t emb_dtype, int
   if (!known_dtype(emb_dtype) || !known_dtype(out_dtype)) return fail(RLT_E_INVAL, "dtype");
   RLT_TRY(check_overlap({matrix_region(out_dev, N, d, ld_out, out_dtype)},
                         {matrix_region(emb_dev, V, d, ld_emb, emb_dtype), vector_region(tok_dev, (int64_t)N * 4)}));
+  ld_emb = row_distance(V, d, ld_emb);
+  ld_out = row_distance(N, d, ld_out);
   RLT_CUDA(embed_lookup(emb_dev, ld_emb, emb_dtype, V, d, tok_dev, N, scale, out_dev, ld_out, out_dtype,
                         (cudaStream_t)stream));
   return ok();
@@ -2046,6 +2055,8 @@ int32_t rlt_op_embed_backward(const void* dout_dev, int64_t ld_dout, int32_t dou
   RLT_TRY(check_overlap({matrix_region(demb_dev, V, d, ld_demb, demb_dtype)},
                         {matrix_region(dout_dev, N, d, ld_dout, dout_dtype), vector_region(tok_dev, (int64_t)N * 4),
                          vector_region(ws_dev, need)}));
+  ld_dout = row_distance(N, d, ld_dout);
+  ld_demb = row_distance(V, d, ld_demb);
   RLT_CUDA(embed_backward(dout_dev, ld_dout, dout_dtype, tok_dev, N, V, d, scale, demb_dev, ld_demb, demb_dtype,
                           accumulate != 0, ws_dev, (cudaStream_t)stream));
   return ok();

@@ -60,3 +60,47 @@ def test_teacher_logits_of_extreme_values(env, T, N, dtype):
     for k in ("loss", "lse", "dh", "dw"):
         within(torch, got[k], ref[k], k)
     assert got["loss"][2] == 0 and got["lse"][2] == 0 and got["lse"][0] != 0
+
+
+# ------------------------------------------------------------------ single rows
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [40, 6504])
+def test_the_distance_of_a_single_row_does_not_matter(env, d, dtype):
+    """With one row there is no other to stand apart from: any ld >= d."""
+    rlt, torch = env
+    h, w, target, weight = make(torch, 1, 1, d, dtype, seed=d, ignored=0.0)
+    h2, w2, _, _ = make(torch, 5, 7, d, dtype, seed=d, ignored=0.0)
+    t5 = torch.zeros(5, dtype=torch.int32, device="cuda")
+    wt5 = torch.ones(5, device="cuda")
+    far = 1 << 59
+    for hh, ww, t, wt in ((h, w, target * 0, weight), (h, w2, target * 0, weight), (h2, w, t5, wt5)):
+        N, V = hh.shape[0], ww.shape[0]
+        want = ce(env, hh, ww, t, wt)
+        a = rlt.Vocab(hh.data_ptr(), far if N == 1 else d, ww.data_ptr(), far if V == 1 else d, N, V, d, int(dtype == "bf16"))
+        out = {"loss": torch.empty(N, device="cuda"), "lse": torch.empty(N, device="cuda"), "dh": torch.empty_like(hh), "dw": torch.empty_like(ww)}
+        ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+        size = ctypes.c_size_t(ws.numel())
+        p = {k: ctypes.c_void_p(x.data_ptr()) for k, x in {**out, "t": t, "wt": wt, "ws": ws}.items()}
+        st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        assert rlt._lib.rlt_op_cross_entropy(ctypes.byref(a), p["t"], p["loss"], p["lse"], p["ws"], ctypes.byref(size), st) == 0
+        size.value = ws.numel()
+        assert rlt._lib.rlt_op_cross_entropy_backward(ctypes.byref(a), p["t"], p["lse"], p["wt"], p["dh"], far if N == 1 else d, p["dw"],
+                                                      far if V == 1 else d, 0, p["ws"], ctypes.byref(size), st) == 0
+        for k in want:
+            assert torch.equal(out[k], want[k]), k
+        if V > 1:
+            continue
+        # the embedding of a table of one row, and its gradient, without ids too
+        tok = torch.tensor([0, -1, 0], dtype=torch.int32, device="cuda")[:1 if N == 1 else 3]
+        e = torch.empty(tok.numel(), d, device="cuda")
+        one = tok.numel() == 1
+        assert rlt._lib.rlt_op_embed(ww.data_ptr(), far, int(dtype == "bf16"), 1, d, tok.data_ptr(), tok.numel(), 2.0, e.data_ptr(),
+                                     far if one else d, 0, st) == 0
+        assert torch.equal(e, torch.where((tok == 0)[:, None], 2 * ww.float(), torch.zeros((), device="cuda")))
+        for n in (tok.numel(), 0):
+            demb = torch.full((1, d), 7.0, device="cuda")
+            size.value = ws.numel()
+            assert rlt._lib.rlt_op_embed_backward(e.data_ptr(), far if n < 2 else d, 0, tok.data_ptr(), n, 1, d, 1.0, demb.data_ptr(), far, 0, 0,
+                                                  p["ws"], ctypes.byref(size), st) == 0
+            want_e = e[tok[:n] == 0] if n else e[:0]
+            assert torch.equal(demb[0], want_e.sum(0))
