@@ -185,7 +185,8 @@ __device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out,
     }
   }
 }
-// One row as two fp16 planes of x * 2^e; returns 2^-e.
+// One row as two fp16 planes of x * 2^e; returns 2^(-e / 2) (e is even: the
+// product of two rows' 2^-e may lie outside fp32 where that of the halves does not).
 __device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __half* out, int64_t plane) {
   const int lane = threadIdx.x & 31;
   const int d8 = vec ? d / 8 : 0;  // groups of eight; what is left goes lane by lane
@@ -206,9 +207,9 @@ __device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __hal
     for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(v[u]));
   }
   m = warp_max(m);
-  // exponent of the largest element; 2^e within the normal numbers
+  // exponent of the largest element, which goes to [2^13, 2^15); 2^e within the normal numbers
   const int top = (int)(__float_as_uint(m) >> 23) - 127;
-  const int e = max(-112, min(126, 14 - top));
+  const int e = max(-112, min(126, 14 - top)) & ~1;
   const float up = __uint_as_float((uint32_t)(127 + e) << 23);
   for (int c0 = lane; c0 < d8; c0 += 32) {
     float v[8];
@@ -242,7 +243,7 @@ __device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __hal
       out[plane + c0 + u * 32] = __float2half_rn(v[u] - __half2float(h));
     }
   }
-  return __uint_as_float((uint32_t)(127 - e) << 23);
+  return __uint_as_float((uint32_t)(127 - e / 2) << 23);
 }
 
 struct Gather {
@@ -271,7 +272,7 @@ struct Gather {
   int64_t w_plane;
   int64_t ld_out;
   int planes;           // bf16 planes (0: none wanted)
-  // fp32: the fp16 planes and their rows' 2^-e, or null
+  // fp32: the fp16 planes and their rows' 2^(-e / 2), or null
   __half *h16, *w16;
   float *h_inv, *w_inv;
 };

@@ -81,7 +81,7 @@ struct Args {
   // STATS, GRAD
   int early;              // operands are older than the kernel before this one: loads do not wait for it
   RowList list;
-  const float *h_inv, *w_inv;  // fp16 planes: 2^-e of the rows of h and w, or null
+  const float *h_inv, *w_inv;  // fp16 planes: 2^(-e / 2) of the rows of h and w, or null
   const int32_t* row_of;  // compact row -> row, or null
   float scale;            // inv_t
   float2* part;           // [2 * n_tiles][part_ld]
@@ -352,8 +352,10 @@ struct Plan : Cut {
 // Each handles up to 128 columns from n_tile * bn + half * 128 of one row per
 // thread, in registers.
 
-// Takes the operands' powers of two back; columns past the matrix are ignored
-// by what follows.
+// Takes the operands' powers of two back, the product of their halves twice:
+// it is a normal number whatever the rows' sizes, so a sum of 0 stays 0 and
+// one that fp32 holds is not lost on the way.  Columns past the matrix are
+// ignored by what follows.
 __device__ __forceinline__ void unscale(const Args& a, int64_t i, bool on, int v0, float (&x)[4][32]) {
   const float hi = on ? a.h_inv[i] : 0.f;
 #pragma unroll
@@ -361,10 +363,9 @@ __device__ __forceinline__ void unscale(const Args& a, int64_t i, bool on, int v
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
       const float4 w = *reinterpret_cast<const float4*>(a.w_inv + v0 + c * 32 + j);
-      x[c][j] *= hi * w.x;
-      x[c][j + 1] *= hi * w.y;
-      x[c][j + 2] *= hi * w.z;
-      x[c][j + 3] *= hi * w.w;
+      const float t[4] = {hi * w.x, hi * w.y, hi * w.z, hi * w.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[c][j + u] = x[c][j + u] * t[u] * t[u];
     }
 }
 

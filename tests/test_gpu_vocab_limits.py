@@ -104,3 +104,44 @@ def test_the_distance_of_a_single_row_does_not_matter(env, d, dtype):
                                                   p["ws"], ctypes.byref(size), st) == 0
             want_e = e[tok[:n] == 0] if n else e[:0]
             assert torch.equal(demb[0], want_e.sum(0))
+
+
+# ------------------------------------------------------------------ fp32 rows of wide range
+def check_all(env, h, w, target, weight, T=1.0):
+    rlt, torch = env
+    got = ce(env, h, w, target, weight)
+    ref = reference(torch, h, w, target=target, weight=weight)
+    for k in ("loss", "lse", "dh", "dw"):
+        within(torch, got[k], ref[k], k)
+    rlt.rlt_check_device()
+    return got
+
+
+@pytest.mark.parametrize("N", [12, 200])
+def test_fp32_rows_of_every_scale(env, N):
+    """Whole rows near the ends of the type, rows of zeros, and products of
+    large rows that have nothing in common (0, not 0 * inf)."""
+    rlt, torch = env
+    V, d = 150, 64
+    h, w, target, weight = make(torch, N, V, d, "f32", seed=N, ignored=0.0)
+    check_all(env, h * 2.0 ** 100, w * 2.0 ** -100, target, weight)
+    check_all(env, h * 2.0 ** -118, w * 2.0 ** 118, target, weight)
+    hz, wz = h.clone(), w.clone()
+    hz[::3], wz[::4] = 0.0, 0.0
+    check_all(env, hz, wz, target, weight)
+    # the columns' halves: rows of h at 2^90 in the first; rows of w at 2^90 in
+    # the second, or at 2^-90 in the first
+    hs, ws = h.clone(), w.clone()
+    hs[:, :32] *= 2.0 ** 90
+    hs[:, 32:] = 0.0
+    ws[::2, 32:] *= 2.0 ** 90
+    ws[::2, :32] = 0.0
+    ws[1::2, :32] *= 2.0 ** -90
+    ws[1::2, 32:] = 0.0
+    got = check_all(env, hs, ws, target, weight)
+    assert not torch.isnan(got["lse"]).any()
+    ids, teacher = make_list(torch, N, V, 9, seed=2)
+    got = kl(env, hs, ws, ids, teacher, 2.0, weight)
+    ref = reference(torch, hs, ws, T=2.0, ids=ids, teacher=teacher, weight=weight)
+    for k in ("loss", "lse", "dh", "dw"):
+        within(torch, got[k], ref[k], k)
