@@ -455,9 +455,12 @@ int32_t rlt_op_sample(const float* logits_dev, int32_t B, int32_t V, const rlt_s
  * whose base is not 16-byte aligned or whose ld % 8 != 0 are copied into the
  * workspace first.  The logits are
  *   z[n][v] = sum_k h[n][k] w[v][k],
- * accumulated in fp32 (fp32 operands to fp32 accuracy, on the tensor cores in
- * 16-bit parts).  They are formed a piece of the vocabulary at a time and
- * never kept. */
+ * accumulated in fp32.  fp32 operands go through the tensor cores in 16-bit
+ * parts and keep the error of an fp32 sum of d products, (2 d + 8) 2^-24 sum_k
+ * |h||w|, whatever sizes the elements of a row have next to each other (a call
+ * with rows that two fp16 parts do not hold takes three bf16 parts and longer);
+ * elements below 2^-110 may be held to 2^-134 only.  The logits are formed a
+ * piece of the vocabulary at a time and never kept. */
 typedef struct rlt_vocab {
   const void* h;     /* [N][d], device */
   int64_t ld_h;

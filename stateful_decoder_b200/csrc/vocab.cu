@@ -185,9 +185,11 @@ __device__ __forceinline__ void copy_row(const T* x, int d, bool vec, bf16* out,
     }
   }
 }
-// One row as two fp16 planes of x * 2^e; returns 2^(-e / 2) (e is even: the
-// product of two rows' 2^-e may lie outside fp32 where that of the halves does not).
-__device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __half* out, int64_t plane) {
+// One row as two fp16 planes, x * 2^e = x0 + 2^-12 x1; returns 2^(-e / 2) (e is
+// even: the product of two rows' 2^-e may lie outside fp32 where that of the
+// halves does not).  *least: the smallest scaled element (Least's bits) of the
+// rows so far, per lane.
+__device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __half* out, int64_t plane, uint32_t* least) {
   const int lane = threadIdx.x & 31;
   const int d8 = vec ? d / 8 : 0;  // groups of eight; what is left goes lane by lane
   float m = 0.f;
@@ -223,10 +225,11 @@ __device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __hal
         if (p == 0) {
           a *= up;
           b *= up;
+          *least = min(*least, min((__float_as_uint(a) & 0x7fffffffu) - 1u, (__float_as_uint(b) & 0x7fffffffu) - 1u));
         }
         h[j] = __floats2half2_rn(a, b);
-        a -= __low2float(h[j]);
-        b -= __high2float(h[j]);
+        a = (a - __low2float(h[j])) * 4096.f;
+        b = (b - __high2float(h[j])) * 4096.f;
       }
       *reinterpret_cast<uint4*>(out + p * plane + c0 * 8) = *reinterpret_cast<const uint4*>(h);
     }
@@ -239,8 +242,9 @@ __device__ __forceinline__ float fp16_row(const float* x, int d, bool vec, __hal
     for (int u = 0; u < 8; ++u) {
       if (c0 + u * 32 >= d) continue;
       const __half h = __float2half_rn(v[u]);
+      *least = min(*least, (__float_as_uint(v[u]) & 0x7fffffffu) - 1u);
       out[c0 + u * 32] = h;
-      out[plane + c0 + u * 32] = __float2half_rn(v[u] - __half2float(h));
+      out[plane + c0 + u * 32] = __float2half_rn((v[u] - __half2float(h)) * 4096.f);
     }
   }
   return __uint_as_float((uint32_t)(127 - e / 2) << 23);
@@ -265,6 +269,7 @@ struct Gather {
   int vec_dh;
   // rows of w to `w_out`
   int w_blocks;
+  int blocks;           // of all three kinds; a smaller grid walks them
   const void* w;
   int64_t ld_w;
   int vec_w;
@@ -275,15 +280,16 @@ struct Gather {
   // fp32: the fp16 planes and their rows' 2^(-e / 2), or null
   __half *h16, *w16;
   float *h_inv, *w_inv;
+  uint32_t *h_least, *w_least;  // per block of rows of h and of w (Least)
 };
 // A row of h or w in all the forms wanted.
 template <typename T>
 __device__ __forceinline__ void convert_row(const T* x, int d, bool vec, bf16* out, int64_t plane, int planes,
-                                            __half* out16, float* inv) {
+                                            __half* out16, float* inv, uint32_t* least) {
   if (planes) copy_row(x, d, vec, out, plane, planes);
   if constexpr (sizeof(T) == 4) {
     if (out16) {
-      const float i = fp16_row(x, d, vec, out16, plane);
+      const float i = fp16_row(x, d, vec, out16, plane, least);
       if ((threadIdx.x & 31) == 0) *inv = i;
     }
   }
@@ -324,11 +330,8 @@ __device__ __forceinline__ int count_rows(const Gather& g, int64_t end, int* red
 // (each counts the rows before its own), blocks that zero the rows behind the
 // last one up to a multiple of 128, blocks that convert w.
 template <typename T>
-__global__ void __launch_bounds__(256, 4) gather_kernel(const Gather g) {
-  griddep_enter();
-  __shared__ int red[8];
+__device__ __forceinline__ void gather_block(const Gather& g, int b, int* red, uint32_t* least) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int b = (int)blockIdx.x;
   if (b < g.row_blocks) {
     const int64_t n0 = (int64_t)b * g.rows_per_block;
     int at = count_rows(g, min((int64_t)g.N, n0), red);
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(256, 4) gather_kernel(const Gather g) {
       if (on) {
         if (lane == 0) g.row_of[i] = (int32_t)n;
         convert_row(static_cast<const T*>(g.h) + n * g.ld_h, g.d, g.vec_h, g.h_out + i * g.ld_out, g.h_plane, g.planes,
-                    g.h16 ? g.h16 + i * g.ld_out : nullptr, g.h_inv + i);
+                    g.h16 ? g.h16 + i * g.ld_out : nullptr, g.h_inv + i, least);
       } else if (n < g.N) {
         if (g.loss && lane == 0) {
           g.loss[n] = 0.f;
@@ -382,7 +385,46 @@ __global__ void __launch_bounds__(256, 4) gather_kernel(const Gather g) {
   const int64_t v = (int64_t)b * 8 + warp;
   if (v < g.V)
     convert_row(static_cast<const T*>(g.w) + v * g.ld_w, g.d, g.vec_w, g.w_out + v * g.ld_out, g.w_plane, g.planes,
-                g.w16 ? g.w16 + v * g.ld_out : nullptr, g.w_inv + v);
+                g.w16 ? g.w16 + v * g.ld_out : nullptr, g.w_inv + v, least);
+}
+template <typename T>
+__global__ void __launch_bounds__(256, 4) gather_kernel(const Gather g) {
+  griddep_enter();
+  __shared__ int red[8];
+  uint32_t least = 0xffffffffu;
+  const int b = (int)blockIdx.x;
+  gather_block<T>(g, b, red, &least);
+  if (sizeof(T) == 4 && (b < g.row_blocks || b >= g.row_blocks + g.pad_blocks)) {
+    least = __reduce_min_sync(0xffffffffu, least);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = (int)least;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 8; ++i) least = min(least, (uint32_t)red[i]);
+      if (b < g.row_blocks) g.h_least[b] = least;
+      else g.w_least[b - g.row_blocks - g.pad_blocks] = least;
+    }
+  }
+}
+// The same into three bf16 planes, if two fp16 planes do not hold the rows; one
+// wave of blocks.
+__global__ void __launch_bounds__(256, 3) gather_again_kernel(const Gather g) {
+  griddep_enter();
+  __shared__ int red[8];
+  __shared__ uint32_t least_s[2][8];
+  uint32_t h = least_of(g.h_least, g.row_blocks, 256), w = least_of(g.w_least, g.w_blocks, 256);
+  h = __reduce_min_sync(0xffffffffu, h);
+  w = __reduce_min_sync(0xffffffffu, w);
+  if ((threadIdx.x & 31) == 0) {
+    least_s[0][threadIdx.x >> 5] = h;
+    least_s[1][threadIdx.x >> 5] = w;
+  }
+  __syncthreads();
+  for (int i = 0; i < 8; ++i) {
+    h = min(h, least_s[0][i]);
+    w = min(w, least_s[1][i]);
+  }
+  if (fp16_holds(h, w, g.d)) return;
+  for (int b = (int)blockIdx.x; b < g.blocks; b += (int)gridDim.x) gather_block<float>(g, b, red, &h);
 }
 
 // Joins the statistics of a row's column groups, in a fixed order, and writes
@@ -542,7 +584,7 @@ __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
 // exchanging halves, after which lane r * NB + n holds z of w row r and h row n.
 // At V = 32000, d = 2048: bf16 29, 31, 39 and 56 us for 1, 2, 4 and 8 rows
 // against 33 on the tensor cores, so up to 2; fp32 53 and 79 us for 4 and 8
-// against 165 (there w is first split into planes), so up to 8.
+// against 172 (there w is first split into planes), so up to 8.
 // Rows of w per group: few, so that the groups spread evenly over the warps
 // (at V = 32000 four per group leave a round 38 % full), but four where each
 // read of h from shared memory has to serve more products.
@@ -793,18 +835,29 @@ cudaError_t set_smem(int bytes) {
   return cudaSuccess;
 }
 
+// The operands of a contraction: A, B, the gradient that GRAD writes or null,
+// and the second form of A and B that some kinds may choose, or null.
+struct Operands {
+  Matrix A, B;
+  const Matrix* G = nullptr;
+  const Matrix *A2 = nullptr, *B2 = nullptr;
+};
 template <int KIND, int CG>
-cudaError_t launch(const Matrix& A, const Matrix& B, const Matrix* G, Args a, cudaStream_t st) {
+cudaError_t launch(const Operands& o, Args a, cudaStream_t st) {
   using C = Cfg<CG>;
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
-  CUtensorMap ta, tb, tg;
+  CUtensorMap ta, tb, tg, ta2, tb2;
   a.stages = std::min(C::MOST_STAGES, C::PIPE / (C::A_BYTES + a.bn / CG * BK * 2));
   // (a box of rows that are not there costs as much as one of rows that are)
   a.a_rows = A_MN ? BM : (int)std::min<int64_t>(BM, round_up(a.M, 8));
-  VOCAB_TRY(tensor_map(&ta, A, A_MN ? 64 : a.a_rows));
-  VOCAB_TRY(tensor_map(&tb, B, B_MN ? 64 : a.bn / CG));
-  if (G) VOCAB_TRY(tensor_map(&tg, *G, 32, 32));
+  VOCAB_TRY(tensor_map(&ta, o.A, A_MN ? 64 : a.a_rows));
+  VOCAB_TRY(tensor_map(&tb, o.B, B_MN ? 64 : a.bn / CG));
+  if (o.G) VOCAB_TRY(tensor_map(&tg, *o.G, 32, 32));
   else tg = ta;
+  if (o.A2) VOCAB_TRY(tensor_map(&ta2, *o.A2, A_MN ? 64 : a.a_rows));
+  else ta2 = ta;
+  if (o.B2) VOCAB_TRY(tensor_map(&tb2, *o.B2, B_MN ? 64 : a.bn / CG));
+  else tb2 = tb;
   VOCAB_TRY((set_smem<vocab_gemm_kernel<KIND, CG>>(C::SMEM)));
   const int64_t tiles = round_up(a.M, BM * CG) / (BM * CG) * (round_up(a.N, a.bn) / a.bn) * a.max_splits;
   if (tiles == 0) return cudaSuccess;
@@ -822,7 +875,7 @@ cudaError_t launch(const Matrix& A, const Matrix& B, const Matrix* G, Args a, cu
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_gemm_kernel<KIND, CG>, ta, tb, tg, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_gemm_kernel<KIND, CG>, ta, tb, tg, ta2, tb2, a);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -830,14 +883,14 @@ cudaError_t launch(const Matrix& A, const Matrix& B, const Matrix* G, Args a, cu
 // Two CTAs per tile (256 rows; each loads half of the columns' operand)
 // wherever there is more than one row tile.
 template <int KIND>
-cudaError_t contract(const Matrix& A, const Matrix& B, const Matrix* G, const Args& a, cudaStream_t st) {
-  return a.M > BM ? launch<KIND, 2>(A, B, G, a, st) : launch<KIND, 1>(A, B, G, a, st);
+cudaError_t contract(const Operands& o, const Args& a, cudaStream_t st) {
+  return a.M > BM ? launch<KIND, 2>(o, a, st) : launch<KIND, 1>(o, a, st);
 }
 
 // Where things lie in the workspace, and how the work is cut.
 struct Layout {
   size_t sid = 0, sq = 0, slogq = 0, some = 0, row_of = 0, count = 0, h = 0, w = 0, h16 = 0, w16 = 0, h_inv = 0,
-         w_inv = 0, part = 0, zsel = 0, g = 0,
+         w_inv = 0, h_least = 0, w_least = 0, part = 0, zsel = 0, g = 0,
          dh = 0, dw = 0, acc = 0, total = 0;
   int planes = 1, terms = 1;      // bf16 planes of h and w; products of h w^T
   int g_planes = 1, g_terms = 1;  // of g, and of its products
@@ -915,6 +968,18 @@ int64_t product_time(int64_t M, int64_t N, int64_t kblocks) {
   return tiles / units * kblocks + rest;
 }
 
+// One wave of blocks gathers rows of h, each of which counts all rows before
+// its own; eight rows of w to a block.
+struct RowBlocks {
+  int per_block, blocks;
+};
+RowBlocks gather_rows(int N) {
+  constexpr int kWave = 4 * kSmCount;
+  const int per_block = (int)round_up(std::max(1, (N + kWave - 1) / kWave), 8);
+  return {per_block, (N + per_block - 1) / per_block};
+}
+int w_gather_blocks(int V) { return (V + 7) / 8; }
+
 Layout layout(const VocabLoss& p, int backward) {
   Layout L;
   auto take = [&](size_t n) {
@@ -949,10 +1014,13 @@ Layout layout(const VocabLoss& p, int backward) {
   }
   if (L.pack_w) L.w = take((size_t)L.planes * p.V * L.ld * 2);
   if (f32 && !L.few) {
-    L.h16 = take((size_t)2 * L.rows * L.ld * 2);
-    L.w16 = take((size_t)2 * p.V * L.ld * 2);
+    // the forward's second form takes the fp16 planes' place
+    L.h16 = take((size_t)(backward ? 2 : 3) * L.rows * L.ld * 2);
+    L.w16 = take((size_t)(backward ? 2 : 3) * p.V * L.ld * 2);
     L.h_inv = take((size_t)L.rows * 4);
     L.w_inv = take((size_t)(round_up(p.V, BN) + BN) * 4);  // tiles read past V
+    L.h_least = take((size_t)gather_rows(p.N).blocks * 4);
+    L.w_least = take((size_t)w_gather_blocks(p.V) * 4);
   }
   const int64_t n_tiles = (p.V + BN - 1) / BN;
   L.bn = logit_columns(p.N, p.V);
@@ -1007,6 +1075,8 @@ struct Prepared {
   const float *h_inv = nullptr, *w_inv = nullptr;
   Matrix h, w;    // of the products of g
   Matrix zh, zw;  // of the logits
+  Matrix zh2, zw2;  // fp32: their second form
+  Least least = {};
 };
 
 int vector_rows(const void* p, int64_t ld, int dtype) {
@@ -1037,10 +1107,9 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
   if (L.gather) {
     g.list = r->list;
     g.weight = weight;
-    // One wave of blocks, each of which counts all rows before its own.
-    constexpr int kWave = 4 * kSmCount;
-    g.rows_per_block = (int)round_up((p.N + kWave - 1) / kWave, 8);
-    g.row_blocks = (p.N + g.rows_per_block - 1) / g.rows_per_block;
+    const RowBlocks rows = gather_rows(p.N);
+    g.rows_per_block = rows.per_block;
+    g.row_blocks = rows.blocks;
     g.pad_blocks = 16;
     g.h = p.h;
     g.ld_h = p.ld_h;
@@ -1059,7 +1128,7 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
     r->zh = r->h = Matrix{g.h_out, L.rows, p.d, L.ld, g.h_plane, L.planes};
   }
   if (L.pack_w) {
-    g.w_blocks = (p.V + 7) / 8;
+    g.w_blocks = w_gather_blocks(p.V);
     g.w = p.w;
     g.ld_w = p.ld_w;
     g.vec_w = vector_rows(p.w, p.ld_w, p.dtype);
@@ -1074,10 +1143,36 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
     r->w_inv = g.w_inv = at<float>(ws, L.w_inv);
     r->zh = Matrix{reinterpret_cast<const bf16*>(g.h16), L.rows, p.d, L.ld, g.h_plane, 2};
     r->zw = Matrix{reinterpret_cast<const bf16*>(g.w16), p.V, p.d, L.ld, g.w_plane, 2};
+    g.h_least = at<uint32_t>(ws, L.h_least);
+    g.w_least = at<uint32_t>(ws, L.w_least);
+    r->least = Least{g.h_least, g.w_least, g.row_blocks, g.w_blocks};
+    r->zh2 = r->h;
+    r->zw2 = r->w;
   }
-  const dim3 grid((unsigned)(g.row_blocks + g.pad_blocks + g.w_blocks));
-  return p.dtype ? launch_pdl(gather_kernel<bf16>, grid, dim3(256), 0, st, g)
-                 : launch_pdl(gather_kernel<float>, grid, dim3(256), 0, st, g);
+  g.blocks = g.row_blocks + g.pad_blocks + g.w_blocks;
+  const dim3 grid((unsigned)g.blocks);
+  if (p.dtype) return launch_pdl(gather_kernel<bf16>, grid, dim3(256), 0, st, g);
+  VOCAB_TRY(launch_pdl(gather_kernel<float>, grid, dim3(256), 0, st, g));
+  if (L.planes) return cudaSuccess;
+  // Forward: the bf16 planes are made only where the fp16 ones do not hold the
+  // rows, in their place, by a launch that else ends at once (2 us).
+  Gather g2 = g;
+  g2.planes = 3;
+  g2.h_out = at<bf16>(ws, L.h16);
+  g2.w_out = at<bf16>(ws, L.w16);
+  g2.h16 = g2.w16 = nullptr;
+  r->zh2 = Matrix{g2.h_out, L.rows, p.d, L.ld, g.h_plane, 3};
+  r->zw2 = Matrix{g2.w_out, p.V, p.d, L.ld, g.w_plane, 3};
+  return launch_pdl(gather_again_kernel, dim3((unsigned)std::min(g.blocks, 3 * kSmCount)), dim3(256), 0, st, g2);
+}
+// The operands of the logits.
+Operands logit_operands(const Prepared& r, const Matrix* G) {
+  Operands o{r.zh, r.zw, G};
+  if (r.least.n_w) {
+    o.A2 = &r.zh2;
+    o.B2 = &r.zw2;
+  }
+  return o;
 }
 
 // k-blocks per tensor-memory sum of the logits.  bf16: 16, an error of some
@@ -1096,7 +1191,8 @@ Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
   Args a{};
   a.terms = L.terms;
   a.chunk = 4;
-  a.fp16 = p.dtype == 0;
+  a.least = r.least;
+  a.terms2 = 6;
   a.h_inv = r.h_inv;
   a.w_inv = r.w_inv;
   a.bn = BN;
@@ -1142,7 +1238,7 @@ cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a
   a.vec = vector_rows(out, ld, p.dtype);
   // bf16 gradients: a sum's drift over 4096 of k (8e-6) is far below their own rounding
   a.chunk = p.dtype ? 64 : 4;
-  VOCAB_TRY(contract<KIND>(G, B, nullptr, a, st));
+  VOCAB_TRY(contract<KIND>(Operands{G, B}, a, st));
   if (a.max_splits == 1) return cudaSuccess;
   const SlabSum s{slab,    a.M,          a.N, a.K,      a.m_count, a.k_count, a.terms,
                   a.units, a.max_splits, cg, a.bn, a.row_of, out,       ld,        accumulate, a.vec,
@@ -1181,7 +1277,8 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
     a.part = part;
     a.part_ld = L.rows;
     a.zsel = zsel;
-    VOCAB_TRY(contract<STATS>(r.zh, r.zw, nullptr, a, st));
+    const Operands z = logit_operands(r, nullptr);
+    VOCAB_TRY(p.dtype ? contract<STATS>(z, a, st) : contract<STATS32>(z, a, st));
   }
   return launch_pdl(join_kernel, dim3((unsigned)((p.N + 31) / 32)), dim3(1024), 0, st, (const float2*)part, L.parts,
                     L.few ? (int64_t)kFewRows : L.rows, p.N, r.row_of, r.count, p.V, r.list, r.slogq,
@@ -1212,12 +1309,12 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.weight = weight;
     a.bn = L.bn;
     a.chunk = logit_chunk(p.dtype, p.N, width, L.bn);
-    VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(r.zh, r.zw, &G, a, st)
-              : L.g_planes == 2 ? contract<GRAD2>(r.zh, r.zw, &G, a, st)
-                                : contract<GRAD3>(r.zh, r.zw, &G, a, st));
+    const Operands z = logit_operands(r, &G);
+    VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(z, a, st)
+              : L.g_planes == 2 ? contract<GRAD2>(z, a, st)
+                                : contract<GRAD3>(z, a, st));
     Args b = args_of(p, L, r);
     b.terms = L.g_terms;
-    b.fp16 = 0;
     if (dh) {
       Args c = b;
       c.M = p.N;

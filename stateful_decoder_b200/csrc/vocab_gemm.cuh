@@ -7,19 +7,26 @@
 // Kinds:
 //   STATS  D = h w^T: per row and up to 128 columns, the maximum and the sum
 //          of exponentials of z = D * inv_t, and z at the row's listed ids
+//   STATS32  the same of fp32 operands, in one of two forms
 //   GRAD   D = h w^T: g = c (exp(z - lse) - q), rounded to bf16
 //   GRAD2, GRAD3  the same as two or three bf16 planes whose sum is g to
-//          2^-16 or 2^-24
+//          2^-16 or 2^-24 (GRAD3: fp32 operands)
 //   DH     D = g w     (A K-major, B MN-major): fp32 partials or typed rows
 //   DW     D = g^T h   (A and B MN-major): fp32 partials or typed rows
 //
-// fp32 operands are held as 16-bit planes whose products add up.  For the
-// logits: two fp16 planes of x * 2^e, e per row so that the row's largest
-// element is near 2^15 (11 + 11 bits and a sign: x to 2^-24 of itself, or
-// 2^-39 of the row's largest); three products, and the powers of two are taken
-// back in the epilogue.  For the products of g, whose columns differ by more
-// than fp16 can hold: three bf16 planes x = x0 + x1 + x2 (24 bits), six
-// products; what is left out is below 2^-24 |x||y|.  Smallest products first.
+// fp32 operands are held as 16-bit planes whose products add up, smallest
+// products first.
+//   Logits: two fp16 planes, x * 2^e = x0 + 2^-12 x1, with e per row so that
+//   the row's largest element is in [2^13, 2^15).  Three products (the two of
+//   x1 are added first, then scaled).  x0 holds x to r = max(2^-11, 2^-25 / x)
+//   of itself, both to max(2^-23, 2^-37 / x); the left-out product of the x1 is
+//   below r_h r_w |h||w|.  The powers of two are taken back in the epilogue.
+//   Logits of rows whose elements differ by more than that holds (fp16_holds):
+//   three bf16 planes x = x0 + x1 + x2, 24 bits of any element (down to 2^-110;
+//   2^-134 is the least that is held), six products, what is left out below
+//   2^-24 |h||w|.  The conversion finds the smallest elements, the contraction
+//   chooses.
+//   Products of g: three bf16 planes, as above.
 //
 // A CTA has twelve warps: two issue TMA, one MMA, one owns tensor memory,
 // eight drain a 128 x 256 accumulator (warps 4-7 its first 128 columns, 8-11
@@ -50,7 +57,7 @@ constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int kThreads = 384;
 constexpr int kNoId = 0x7fffffff;
 
-enum Kind { STATS, GRAD, GRAD2, GRAD3, DH, DW };
+enum Kind { STATS, STATS32, GRAD, GRAD2, GRAD3, DH, DW };
 
 // A row's list of (id, probability) as the kernels see it.
 struct RowList {
@@ -65,12 +72,45 @@ __device__ __forceinline__ bool takes_part(const RowList& r, int64_t n, int V) {
   return id >= 0 && id < V;
 }
 
+// The smallest nonzero elements of scaled fp32 rows, per block of the
+// conversion, as the bits of |x| less one (so that 0 is the largest).
+struct Least {
+  const uint32_t *h, *w;
+  int n_h, n_w;
+};
+// This thread's share of them, four words to a load and all loads of a few
+// thousand words in flight.
+__device__ __forceinline__ uint32_t least_of(const uint32_t* p, int n, int threads) {
+  uint32_t r = 0xffffffffu;
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n / 4; i += threads) {
+    const uint4 v = q[i];
+    r = min(r, min(min(v.x, v.y), min(v.z, v.w)));
+  }
+  if ((int)threadIdx.x < n % 4) r = min(r, p[n / 4 * 4 + threadIdx.x]);
+  return r;
+}
+// Do two fp16 planes hold every product of such rows to d / 2 roundings of
+// fp32, as many as a sum of d products has in any case?  With m the smallest
+// element, or 2^-14 where that is more: m_h m_w >= 2^-25 / d bounds the left-out
+// product by 2^-50 / (m_h m_w) <= (d / 2) 2^-24, and each operand's own error by
+// 2^-37 / m <= (d / 4) 2^-24.  Rows of random numbers have it so (32,000 and
+// 16,384 normal rows of 2,048: all but about 1 call in 100), rows with outliers
+// 2^20 and more above the rest do not.
+__device__ __forceinline__ bool fp16_holds(uint32_t h, uint32_t w, int d) {
+  const float mh = h == 0xffffffffu ? 0x1p-14f : fminf(__uint_as_float(h + 1), 0x1p-14f);
+  const float mw = w == 0xffffffffu ? 0x1p-14f : fminf(__uint_as_float(w + 1), 0x1p-14f);
+  return mh * mw * (float)d >= 0x1p-25f;
+}
+
 struct Args {
   int M, N, K;            // extents; *m_count / *k_count replace M / K where set
   const int32_t* m_count;
   const int32_t* k_count;
   int terms;              // 1, 2, 3 or 6 plane products
-  int fp16;               // the operands' type: bf16 or fp16
+  Least least;            // STATS32, GRAD3: decide between two fp16 planes in `terms` products
+  int terms2;             // and the operands' second form, three bf16 planes in terms2
   int chunk;              // k-blocks per tensor-memory sum (of the leading term)
   int bn;                 // columns per tile: a multiple of 64 (DH, DW: 64 per CTA) up to BN
   int stages;             // of bn's size
@@ -81,7 +121,7 @@ struct Args {
   // STATS, GRAD
   int early;              // operands are older than the kernel before this one: loads do not wait for it
   RowList list;
-  const float *h_inv, *w_inv;  // fp16 planes: 2^(-e / 2) of the rows of h and w, or null
+  const float *h_inv, *w_inv;  // fp16 planes: 2^(-e / 2) of the rows of h and w
   const int32_t* row_of;  // compact row -> row, or null
   float scale;            // inv_t
   float2* part;           // [2 * n_tiles][part_ld]
@@ -318,8 +358,8 @@ constexpr int kPanel = 16;  // row tiles of 128 per panel
 
 template <int CG>
 struct Plan : Cut {
-  __device__ __forceinline__ void init(const Args& a) {
-    Cut::init(a.m_count ? *a.m_count : a.M, a.N, a.k_count ? *a.k_count : a.K, BM * CG, a.bn, a.terms, a.units,
+  __device__ __forceinline__ void init(const Args& a, int terms) {
+    Cut::init(a.m_count ? *a.m_count : a.M, a.N, a.k_count ? *a.k_count : a.K, BM * CG, a.bn, terms, a.units,
               a.max_splits);
   }
   __device__ __forceinline__ Tile at(int t) const {
@@ -341,8 +381,8 @@ struct Plan : Cut {
   }
   // End of the tensor-memory sum that starts at c0.  Of several plane products
   // all but the last add up to 2^-8 of it, and their error counts as little.
-  __device__ __forceinline__ int chunk_end(const Args& a, int c0, int kb1) const {
-    const int small = (a.terms - 1) * kb;
+  __device__ __forceinline__ int chunk_end(const Args& a, int terms, int c0, int kb1) const {
+    const int small = (terms - 1) * kb;
     if (c0 < small) return min(kb1, min(c0 + 64, small));
     return min(kb1, c0 + a.chunk);
   }
@@ -352,6 +392,15 @@ struct Plan : Cut {
 // Each handles up to 128 columns from n_tile * bn + half * 128 of one row per
 // thread, in registers.
 
+// x *= (h w)^2 for two columns, in packed operations.
+__device__ __forceinline__ void scale2(float& x0, float& x1, float h, float w0, float w1) {
+  asm("{\n\t.reg .b64 x, t, h;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 h, {%2, %2};\n\tmov.b64 t, {%3, %4};\n\t"
+      "mul.rn.f32x2 t, t, h;\n\tmul.rn.f32x2 x, x, t;\n\tmul.rn.f32x2 x, x, t;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(h), "f"(w0), "f"(w1));
+}
 // Takes the operands' powers of two back, the product of their halves twice:
 // it is a normal number whatever the rows' sizes, so a sum of 0 stays 0 and
 // one that fp32 holds is not lost on the way.  Columns past the matrix are
@@ -363,9 +412,8 @@ __device__ __forceinline__ void unscale(const Args& a, int64_t i, bool on, int v
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
       const float4 w = *reinterpret_cast<const float4*>(a.w_inv + v0 + c * 32 + j);
-      const float t[4] = {hi * w.x, hi * w.y, hi * w.z, hi * w.w};
-#pragma unroll
-      for (int u = 0; u < 4; ++u) x[c][j + u] = x[c][j + u] * t[u] * t[u];
+      scale2(x[c][j], x[c][j + 1], hi, w.x, w.y);
+      scale2(x[c][j + 2], x[c][j + 3], hi, w.z, w.w);
     }
 }
 
@@ -557,9 +605,11 @@ __device__ __forceinline__ void product_epilogue(const Args& a, uint32_t stage, 
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmG, const Args a) {
+                      const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmA2,
+                      const __grid_constant__ CUtensorMap tmB2, const Args a) {
   using C = Cfg<CG>;
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
+  constexpr bool kChooses = KIND == STATS32 || KIND == GRAD3;  // between two forms of fp32 operands
   const int S = a.stages;
   const uint32_t stage_bytes = C::A_BYTES + (uint32_t)a.bn / CG * (BK * 2);
   extern __shared__ uint8_t smem_raw[];
@@ -596,13 +646,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!a.early) griddep_enter();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  bool second = false;
+  if constexpr (kChooses) {
+    __shared__ uint32_t least[2][kThreads / 32];
+    uint32_t h = least_of(a.least.h, a.least.n_h, kThreads), w = least_of(a.least.w, a.least.n_w, kThreads);
+    h = __reduce_min_sync(0xffffffffu, h);
+    w = __reduce_min_sync(0xffffffffu, w);
+    if (lane == 0) {
+      least[0][warp] = h;
+      least[1][warp] = w;
+    }
+    __syncthreads();
+    h = __reduce_min_sync(0xffffffffu, least[0][min(lane, kThreads / 32 - 1)]);
+    w = __reduce_min_sync(0xffffffffu, least[1][min(lane, kThreads / 32 - 1)]);
+    second = __any_sync(0xffffffffu, !fp16_holds(h, w, a.K));  // a vote: uniform
+  } else {
+    __syncthreads();
+  }
   if (a.early && warp >= 4) griddep_enter();
   if constexpr (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
   Plan<CG> plan;
-  plan.init(a);
+  const int terms = kChooses && second ? a.terms2 : a.terms;
+  plan.init(a, terms);
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   // The loops below run in whole warps with one elected lane at work: what
@@ -616,10 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (0,0), or the last three, or (1,0) (0,0); `planes` lists an operand's,
     // last product lowest.
     const bool is_a = warp == 0;
-    const uint32_t planes = a.terms == 6   ? (is_a ? 0x201100u : 0x021010u)
-                            : a.terms == 3 ? (is_a ? 0x100u : 0x010u)
-                            : a.terms == 2 ? (is_a ? 0x10u : 0u)
-                                           : 0u;
+    const uint32_t planes = terms == 6   ? (is_a ? 0x201100u : 0x021010u)
+                            : terms == 3 ? (is_a ? 0x100u : 0x010u)
+                            : terms == 2 ? (is_a ? 0x10u : 0u)
+                                         : 0u;
     int slot = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -635,14 +702,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         __syncwarp();
-        const int plane = (planes >> (4 * (a.terms - 1 - turn))) & 15;
+        const int plane = (planes >> (4 * (terms - 1 - turn))) & 15;
         const uint32_t sa = base + slot * stage_bytes;
         uint32_t bar = full + 8 * slot;
         if (elect_one()) {
           if (is_a && rank == 0) mbar_arrive_expect_tx(bar, bytes);
           if constexpr (CG == 2) bar = in_leader(bar);
-          if (is_a) load_tile<CG, A_MN>(sa, &tmA, bar, BM, row, kt * BK + k_off, plane);
-          else load_tile<CG, B_MN>(sa + C::A_BYTES, &tmB, bar, a.bn / CG, row, kt * BK + k_off, plane);
+          if (is_a) load_tile<CG, A_MN>(sa, kChooses && second ? &tmA2 : &tmA, bar, BM, row, kt * BK + k_off, plane);
+          else load_tile<CG, B_MN>(sa + C::A_BYTES, kChooses && second ? &tmB2 : &tmB, bar, a.bn / CG, row, kt * BK + k_off, plane);
         }
         __syncwarp();
         issued = min(S, issued + 1);
@@ -663,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1 && rank == 0) {
-    const uint32_t idesc = (1u << 4) | (a.fp16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
+    const uint32_t idesc = (1u << 4) | (kChooses && !second ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
                            ((uint32_t)(a.bn >> 3) << 17) | ((uint32_t)(BM * CG >> 4) << 24);
     int slot = 0;
     uint32_t phase = 0, n_acc = 0;
@@ -671,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = first; t < plan.tiles && ok; t += step) {
       const Tile tile = plan.at(t);
       for (int c0 = tile.kb0, c1; c0 < tile.kb1 && ok; c0 = c1, ++n_acc) {
-        c1 = plan.chunk_end(a, c0, tile.kb1);
+        c1 = plan.chunk_end(a, terms, c0, tile.kb1);
         const uint32_t as = n_acc & 1u;
         if (!mbar_wait(acc_empty + 8 * as, ((n_acc >> 1) & 1u) ^ 1u)) {
           ok = false;
@@ -725,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) x[c][j] = 0.f;
       }
-      for (int c0 = tile.kb0; c0 < tile.kb1; c0 = plan.chunk_end(a, c0, tile.kb1), ++n_acc) {
+      for (int c0 = tile.kb0; c0 < tile.kb1; c0 = plan.chunk_end(a, terms, c0, tile.kb1), ++n_acc) {
         const uint32_t as = n_acc & 1u;
         if (!mbar_wait(acc_full + 8 * as, (n_acc >> 1) & 1u)) {
           ok = false;
@@ -734,6 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + as * BN + lanes + half * 128;
+        // fp16: the sum of x1's products, complete, is scaled by 2^-12 as the leading product's joins it
+        float keep = 1.f;
+        if constexpr (kChooses) keep = !second && c0 == (terms - 1) * plan.kb ? 1.f / 4096 : 1.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           float v[16];
@@ -743,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 16; ++j) x[c >> 1][(c & 1) * 16 + j] = v[j];
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[c >> 1][(c & 1) * 16 + j] += v[j];
+            for (int j = 0; j < 16; ++j) x[c >> 1][(c & 1) * 16 + j] = kChooses ? fmaf(x[c >> 1][(c & 1) * 16 + j], keep, v[j]) : x[c >> 1][(c & 1) * 16 + j] + v[j];
           }
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -754,10 +824,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if constexpr (KIND == STATS || KIND == GRAD3) {
-        if (a.h_inv) unscale(a, i, on, v0, x);
+      if constexpr (kChooses) {
+        if (!second) unscale(a, i, on, v0, x);
       }
-      if constexpr (KIND == STATS) stats_epilogue(a, i, n, on, tile.n, half, v0, pos, x);
+      if constexpr (KIND == STATS || KIND == STATS32) stats_epilogue(a, i, n, on, tile.n, half, v0, pos, x);
       else if constexpr (KIND != DH && KIND != DW)
         grad_epilogue<KIND == GRAD ? 1 : KIND == GRAD2 ? 2 : 3>(
             a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n, on, tile.n, half, v0, pos, x);

@@ -4,9 +4,9 @@ gradient, each with its masks, strides, odd sizes, streams and graphs.
 
 Tolerances.  Every bound is elementwise and follows from the arithmetic, with
 u = 2^-24 (fp32) and half a bf16 step 2^-8:
-  logits     a sum of d fp32 products in any order, the fp32 operands taken as
-             three bf16 parts of which products below 2^-23 |h||w| are left
-             out: |dz| <= (2 d + 8) u sum|h||w|
+  logits     a sum of d fp32 products in any order, and as much again for fp32
+             operands taken as 16-bit parts, whose own error and left-out
+             products are below (d + 8) u |h||w|: |dz| <= (2 d + 8) u sum|h||w|
   lse        2 |dz| plus the exponentials' and sums' own (1024 + 4 |z|) u
   p          relative: |dz| + |dlse| + (8 + 2 |z - lse|) u
   dz         c p dp, plus one rounding to bf16 (bf16 operands) or to three

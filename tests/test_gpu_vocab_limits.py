@@ -145,3 +145,83 @@ def test_fp32_rows_of_every_scale(env, N):
     ref = reference(torch, hs, ws, T=2.0, ids=ids, teacher=teacher, weight=weight)
     for k in ("loss", "lse", "dh", "dw"):
         within(torch, got[k], ref[k], k)
+
+
+@pytest.mark.parametrize("N", [5, 9, 130, 300])
+@pytest.mark.parametrize("power", [20, 27, 33, 60, 100])
+@pytest.mark.parametrize("side,d", [("h", 64), ("w", 64), ("both", 64), ("both", 1040)])
+def test_fp32_outlier_columns(env, side, d, power, N):
+    """A column that is large in one operand where the other has none: the
+    logits come from the elements far below the row's largest, to the accuracy
+    of an fp32 sum of products all the same; with both, from products of two
+    such elements."""
+    rlt, torch = env
+    h, w, target, weight = make(torch, N, 333, d, "f32", seed=N + power, ignored=0.0)
+    if side != "w":
+        h[:, 5], w[:, 5] = 2.0 ** power, 0.0
+        h[0, 17], w[:, 17] = 2.0 ** power, 0.0
+    if side != "h":
+        w[:, 9], h[:, 9] = 2.0 ** power, 0.0
+        w[0, 30], h[:, 30] = -2.0 ** power, 0.0
+    check_all(env, h, w, target, weight)
+
+
+def test_fp32_rows_with_elements_of_every_size(env):
+    """Elements from 2^-60 to 2^60 of the row's typical one, met by their
+    inverses; and the pair whose small elements carry the product."""
+    rlt, torch = env
+    N, V, d = 40, 200, 96
+    h, w, target, weight = make(torch, N, V, d, "f32", seed=5, ignored=0.0)
+    s = torch.exp2(torch.linspace(-60, 60, d, device="cuda").round())
+    check_all(env, h * s, w / s, target, weight)
+    h, w = torch.zeros(9, 2, device="cuda"), torch.zeros(3, 2, device="cuda")
+    h[:, 0], h[:, 1] = 1.0, 3.1e-10
+    w[:, 0], w[:, 1] = 2.7e-10, torch.tensor([1.234, -0.5, 0.25], device="cuda")
+    target = torch.tensor([0, 1, 2] * 3, dtype=torch.int32, device="cuda")
+    got = check_all(env, h, w, target, torch.ones(9, device="cuda"))
+    assert not torch.isnan(got["lse"]).any()
+
+
+def test_fp32_wide_rows_over_several_pieces(env):
+    """The backward walks the vocabulary in pieces; one wide row of w, in the
+    last of them."""
+    rlt, torch = env
+    N, V, d = 44000, 4999, 16
+    h, w, target, weight = make(torch, N, V, d, "f32", seed=6)
+    weight /= N
+    h[:, 3], w[:, 3] = 0.0, 0.0
+    w[V - 2, 3] = 2.0 ** 70
+    w[V - 2, 7] = 1.0
+    h[:, 7] = 2.0 ** -3
+    got = ce(env, h, w, target, weight)
+    dw = [0.0, 0.0]
+    for i in range(0, N, 11000):
+        s = slice(i, i + 11000)
+        ref = reference(torch, h[s], w, target=target[s], weight=weight[s])
+        for k in ("loss", "lse", "dh"):
+            within(torch, got[k][s], ref[k], k)
+        dw[0] = dw[0] + ref["dw"][0]
+        dw[1] = dw[1] + ref["dw"][1] * 4  # (2 n + 8) u counts all N terms
+    within(torch, got["dw"], dw, "dw")
+
+
+def test_fp32_wide_rows_in_a_replayed_graph(env):
+    """The kernels choose by the values they are given: captured on ordinary
+    rows, replayed on wide ones and back, with an eager call's bits."""
+    rlt, torch = env
+    h, w, target, weight = make(torch, 150, 400, 48, "f32", seed=16, ignored=0.0)
+    h2, w2 = h.clone(), w.clone()
+    h2[:, 5], w2[:, 5] = 2.0 ** 80, 0.0
+    a, b = h.clone(), w.clone()
+    ce(env, a, b, target, weight)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ce(env, a, b, target, weight)
+    for x, y in ((h2, w2), (h, w), (h2, w2)):
+        a.copy_(x)
+        b.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = check_all(env, a, b, target, weight)
+        for k in out:
+            assert torch.equal(out[k], eager[k]), k
