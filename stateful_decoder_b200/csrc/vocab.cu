@@ -496,7 +496,8 @@ struct SlabSum {
   const float4* slab;
   int M, N, K;
   const int32_t *m_count, *k_count;
-  int terms, units, max_splits, cg, bn;
+  int terms, terms2, fine_rows, units, max_splits, cg, bn;  // as in Args
+  int rows_in_k;  // the rows that take part run along K (DW), not M
   const int32_t* row_of;
   void* out;
   int64_t ld;
@@ -510,7 +511,8 @@ __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
   const int M = a.m_count ? *a.m_count : a.M, K = a.k_count ? *a.k_count : a.K;
   const int tile_rows = BM * a.cg;
   Cut cut;
-  cut.init(M, a.N, K, tile_rows, a.bn, a.terms, a.units, a.max_splits);
+  const int terms = (a.rows_in_k ? K : M) <= a.fine_rows ? a.terms2 : a.terms;
+  cut.init(M, a.N, K, tile_rows, a.bn, terms, a.units, a.max_splits);
   const int rows = min(M, tile_rows);  // of a tile, that exist
   const int total = cut.rest * rows * (BN / 8), tile = tile_rows * (BN / 4);
   const int64_t stride = (int64_t)cut.rest * tile;
@@ -836,7 +838,8 @@ cudaError_t set_smem(int bytes) {
 }
 
 // The operands of a contraction: A, B, the gradient that GRAD writes or null,
-// and the second form of A and B that some kinds may choose, or null.
+// and the second form of A (GRAD: of the gradient) and B that some kinds may
+// choose, or null.
 struct Operands {
   Matrix A, B;
   const Matrix* G = nullptr;
@@ -854,7 +857,7 @@ cudaError_t launch(const Operands& o, Args a, cudaStream_t st) {
   VOCAB_TRY(tensor_map(&tb, o.B, B_MN ? 64 : a.bn / CG));
   if (o.G) VOCAB_TRY(tensor_map(&tg, *o.G, 32, 32));
   else tg = ta;
-  if (o.A2) VOCAB_TRY(tensor_map(&ta2, *o.A2, A_MN ? 64 : a.a_rows));
+  if (o.A2) VOCAB_TRY(KIND == GRAD ? tensor_map(&ta2, *o.A2, 32, 32) : tensor_map(&ta2, *o.A2, A_MN ? 64 : a.a_rows));
   else ta2 = ta;
   if (o.B2) VOCAB_TRY(tensor_map(&tb2, *o.B2, B_MN ? 64 : a.bn / CG));
   else tb2 = tb;
@@ -904,6 +907,7 @@ struct Layout {
 bool tma_ready(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
 
 constexpr int kMostSplits = 64;
+constexpr int kFineRows = 256;  // a multiple of the rows of a tile
 int cta_group(int M) { return M > BM ? 2 : 1; }
 // Floats that the split sums of a product can take: split_rule makes at most
 // two rounds of split tiles, and none of fewer than 32 k-blocks.
@@ -1033,9 +1037,10 @@ Layout layout(const VocabLoss& p, int backward) {
   // g of bf16 operands is rounded to bf16 as an operand of the products, about
   // as much again as the gradients' own rounding (1.41 of it in all, over many
   // rows).  Over few rows single entries of g carry the gradients and their
-  // rounding does not average: up to 256 rows a second plane takes it away, at
-  // 13 to 22 % of the backward's time (64 to 256 rows, V = 32000, d = 2048).
-  L.g_planes = f32 ? 3 : p.N <= 256 ? 2 : 1;
+  // rounding does not average: where up to kFineRows take part, a count that
+  // only the device knows, a second plane takes it away, at 13 to 22 % of the
+  // backward's time (64 to 256 rows, V = 32000, d = 2048).
+  L.g_planes = f32 ? 3 : p.N <= kFineRows ? 2 : 1;  // at most, and what the cut of the work reckons with
   L.g_terms = f32 ? 6 : L.g_planes;
   // The piece: at most as wide as 512 MB of g allow (256 MB was 5 % slower at
   // 16,368 rows, 1 GB no faster), at least 2048 columns, and of the next few
@@ -1055,7 +1060,7 @@ Layout layout(const VocabLoss& p, int backward) {
       L.pieces = (int)pieces;
     }
   }
-  L.g = take((size_t)L.g_planes * L.rows * L.piece * 2);
+  L.g = take((size_t)(f32 ? 3 * L.rows : std::max<int64_t>(L.rows, 2 * kFineRows)) * L.piece * 2);
   L.dw = take((size_t)slab_floats(L.piece, p.d, L.rows / BK * L.g_terms, &L.dw_splits) * 4);
   L.dh = take((size_t)slab_floats(p.N, p.d, (int64_t)L.piece / BK * L.g_terms, &L.dh_splits) * 4);
   if (L.pieces > 1) L.acc = take((size_t)L.rows * p.d * 4);  // dh over the pieces
@@ -1225,7 +1230,7 @@ cudaError_t few_rows_of(const VocabLoss& p, const Layout& L, const RowList& list
 
 // A product of g into typed rows, K split where the rule says so.
 template <int KIND>
-cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a, float4* slab, void* out, int64_t ld,
+cudaError_t product(const VocabLoss& p, const Operands& o, Args a, float4* slab, void* out, int64_t ld,
                     int accumulate, cudaStream_t st) {
   const int cg = cta_group(a.M);
   a.units = kSmCount / cg;
@@ -1238,11 +1243,11 @@ cudaError_t product(const VocabLoss& p, const Matrix& G, const Matrix& B, Args a
   a.vec = vector_rows(out, ld, p.dtype);
   // bf16 gradients: a sum's drift over 4096 of k (8e-6) is far below their own rounding
   a.chunk = p.dtype ? 64 : 4;
-  VOCAB_TRY(contract<KIND>(Operands{G, B}, a, st));
+  VOCAB_TRY(contract<KIND>(o, a, st));
   if (a.max_splits == 1) return cudaSuccess;
-  const SlabSum s{slab,    a.M,          a.N, a.K,      a.m_count, a.k_count, a.terms,
-                  a.units, a.max_splits, cg, a.bn, a.row_of, out,       ld,        accumulate, a.vec,
-                  a.acc,   a.acc_in,     a.acc_out};
+  const SlabSum s{slab,  a.M,    a.N,          a.K, a.m_count, a.k_count,  a.terms,  a.terms2, a.fine_rows,
+                  a.units, a.max_splits, cg, a.bn, KIND == DW, a.row_of,  out, ld,       accumulate,
+                  a.vec, a.acc,  a.acc_in,     a.acc_out};
   const int64_t tiles = (a.M + BM * cg - 1) / (BM * cg) * (int64_t)((a.N + a.bn - 1) / a.bn);
   const int64_t most = std::min<int64_t>(tiles, a.units) * std::min(a.M, BM * cg) * (BN / 8);
   const dim3 grid((unsigned)std::min<int64_t>(4 * kSmCount, (most + 255) / 256));
@@ -1296,7 +1301,10 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
   Prepared r;
   VOCAB_TRY(prepare(p, L, ws, weight, nullptr, nullptr, dh, ld_dh, &r, st));
   float4 *dh_slab = at<float4>(ws, L.dh), *dw_slab = at<float4>(ws, L.dw);
-  const Matrix G{at<bf16>(ws, L.g), L.rows, L.piece, L.piece, L.rows * L.piece, L.g_planes};
+  // g: three planes of fp32 operands; of bf16 ones a single plane, or two of kFineRows in its place
+  const Matrix G{at<bf16>(ws, L.g), L.rows, L.piece, L.piece, L.rows * L.piece, p.dtype ? 1 : 3};
+  const Matrix G2{G.p, kFineRows, L.piece, L.piece, (int64_t)kFineRows * L.piece, 2};
+  const Matrix* fine = p.dtype ? &G2 : nullptr;
   for (int i = 0; i < L.pieces; ++i) {
     const int v0 = i * L.piece, width = std::min(p.V - v0, L.piece);
     Args a = args_of(p, L, r);
@@ -1309,12 +1317,14 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.weight = weight;
     a.bn = L.bn;
     a.chunk = logit_chunk(p.dtype, p.N, width, L.bn);
-    const Operands z = logit_operands(r, &G);
-    VOCAB_TRY(L.g_planes == 1   ? contract<GRAD>(z, a, st)
-              : L.g_planes == 2 ? contract<GRAD2>(z, a, st)
-                                : contract<GRAD3>(z, a, st));
+    a.fine_rows = fine ? kFineRows : 0;
+    Operands z = logit_operands(r, &G);
+    if (fine) z.A2 = fine;
+    VOCAB_TRY(p.dtype ? contract<GRAD>(z, a, st) : contract<GRAD3>(z, a, st));
     Args b = args_of(p, L, r);
-    b.terms = L.g_terms;
+    b.terms = fine ? 1 : 6;
+    b.terms2 = 2;
+    b.fine_rows = a.fine_rows;
     if (dh) {
       Args c = b;
       c.M = p.N;
@@ -1326,7 +1336,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
       c.acc = L.pieces > 1 ? at<float>(ws, L.acc) : nullptr;
       c.acc_in = i > 0;
       c.acc_out = i + 1 < L.pieces;
-      VOCAB_TRY(product<DH>(p, G, r.w, c, dh_slab, dh, ld_dh, 0, st));
+      VOCAB_TRY(product<DH>(p, Operands{G, r.w, nullptr, fine}, c, dh_slab, dh, ld_dh, 0, st));
     }
     if (dw) {
       b.row_of = nullptr;
@@ -1335,7 +1345,7 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
       b.K = p.N;
       b.k_count = r.count;
       b.max_splits = L.dw_splits;
-      VOCAB_TRY(product<DW>(p, G, r.h, b, dw_slab, static_cast<uint8_t*>(dw) + (int64_t)v0 * ld_dw * e, ld_dw,
+      VOCAB_TRY(product<DW>(p, Operands{G, r.h, nullptr, fine}, b, dw_slab, static_cast<uint8_t*>(dw) + (int64_t)v0 * ld_dw * e, ld_dw,
                             accumulate_dw, st));
     }
   }

@@ -8,9 +8,9 @@
 //   STATS  D = h w^T: per row and up to 128 columns, the maximum and the sum
 //          of exponentials of z = D * inv_t, and z at the row's listed ids
 //   STATS32  the same of fp32 operands, in one of two forms
-//   GRAD   D = h w^T: g = c (exp(z - lse) - q), rounded to bf16
-//   GRAD2, GRAD3  the same as two or three bf16 planes whose sum is g to
-//          2^-16 or 2^-24 (GRAD3: fp32 operands)
+//   GRAD   D = h w^T of bf16 operands: g = c (exp(z - lse) - q), rounded to
+//          bf16, or as two planes whose sum is g to 2^-16 (Args::fine_rows)
+//   GRAD3  the same of fp32 operands, as three planes, g to 2^-24
 //   DH     D = g w     (A K-major, B MN-major): fp32 partials or typed rows
 //   DW     D = g^T h   (A and B MN-major): fp32 partials or typed rows
 //
@@ -57,7 +57,7 @@ constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int kThreads = 384;
 constexpr int kNoId = 0x7fffffff;
 
-enum Kind { STATS, STATS32, GRAD, GRAD2, GRAD3, DH, DW };
+enum Kind { STATS, STATS32, GRAD, GRAD3, DH, DW };
 
 // A row's list of (id, probability) as the kernels see it.
 struct RowList {
@@ -109,8 +109,10 @@ struct Args {
   const int32_t* m_count;
   const int32_t* k_count;
   int terms;              // 1, 2, 3 or 6 plane products
-  Least least;            // STATS32, GRAD3: decide between two fp16 planes in `terms` products
-  int terms2;             // and the operands' second form, three bf16 planes in terms2
+  // A second form of an operand, in terms2 products, that the device chooses:
+  int terms2;
+  Least least;            // STATS32, GRAD3: three bf16 planes for two fp16 ones
+  int fine_rows;          // GRAD, DH, DW: g is two planes, not one, where at most so many rows take part
   int chunk;              // k-blocks per tensor-memory sum (of the leading term)
   int bn;                 // columns per tile: a multiple of 64 (DH, DW: 64 per CTA) up to BN
   int stages;             // of bn's size
@@ -605,11 +607,14 @@ __device__ __forceinline__ void product_epilogue(const Args& a, uint32_t stage, 
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmA2,
+                      const __grid_constant__ CUtensorMap tmG,
+                      const __grid_constant__ CUtensorMap tmA2,  // second forms; GRAD: of G
                       const __grid_constant__ CUtensorMap tmB2, const Args a) {
   using C = Cfg<CG>;
   constexpr bool A_MN = KIND == DW, B_MN = KIND == DH || KIND == DW;
   constexpr bool kChooses = KIND == STATS32 || KIND == GRAD3;  // between two forms of fp32 operands
+  constexpr bool kFine = KIND == GRAD || KIND == DH || KIND == DW;  // between two of g
+  constexpr bool kSecondA = kChooses || KIND == DH || KIND == DW, kSecondB = kChooses;
   const int S = a.stages;
   const uint32_t stage_bytes = C::A_BYTES + (uint32_t)a.bn / CG * (BK * 2);
   extern __shared__ uint8_t smem_raw[];
@@ -662,13 +667,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     second = __any_sync(0xffffffffu, !fp16_holds(h, w, a.K));  // a vote: uniform
   } else {
     __syncthreads();
+    if constexpr (kFine) {
+      const int32_t* count = KIND == DW ? a.k_count : a.m_count;  // rows that take part
+      second = __any_sync(0xffffffffu, a.fine_rows > 0 && *count <= a.fine_rows);
+    }
   }
   if (a.early && warp >= 4) griddep_enter();
   if constexpr (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
   Plan<CG> plan;
-  const int terms = kChooses && second ? a.terms2 : a.terms;
+  const int terms = kSecondA && second ? a.terms2 : a.terms;
   plan.init(a, terms);
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
@@ -708,8 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           if (is_a && rank == 0) mbar_arrive_expect_tx(bar, bytes);
           if constexpr (CG == 2) bar = in_leader(bar);
-          if (is_a) load_tile<CG, A_MN>(sa, kChooses && second ? &tmA2 : &tmA, bar, BM, row, kt * BK + k_off, plane);
-          else load_tile<CG, B_MN>(sa + C::A_BYTES, kChooses && second ? &tmB2 : &tmB, bar, a.bn / CG, row, kt * BK + k_off, plane);
+          if (is_a) load_tile<CG, A_MN>(sa, kSecondA && second ? &tmA2 : &tmA, bar, BM, row, kt * BK + k_off, plane);
+          else load_tile<CG, B_MN>(sa + C::A_BYTES, kSecondB && second ? &tmB2 : &tmB, bar, a.bn / CG, row, kt * BK + k_off, plane);
         }
         __syncwarp();
         issued = min(S, issued + 1);
@@ -828,9 +837,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!second) unscale(a, i, on, v0, x);
       }
       if constexpr (KIND == STATS || KIND == STATS32) stats_epilogue(a, i, n, on, tile.n, half, v0, pos, x);
-      else if constexpr (KIND != DH && KIND != DW)
-        grad_epilogue<KIND == GRAD ? 1 : KIND == GRAD2 ? 2 : 3>(
-            a, &tmG, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, i - lane, lane, n, on, tile.n, half, v0, pos, x);
+      else if constexpr (KIND != DH && KIND != DW) {
+        const uint32_t stage = base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096;
+        if constexpr (KIND == GRAD3) grad_epilogue<3>(a, &tmG, stage, i - lane, lane, n, on, tile.n, half, v0, pos, x);
+        else if (second) grad_epilogue<2>(a, &tmA2, stage, i - lane, lane, n, on, tile.n, half, v0, pos, x);
+        else grad_epilogue<1>(a, &tmG, stage, i - lane, lane, n, on, tile.n, half, v0, pos, x);
+      }
       else {
         float4* slab_row = tile.split < 0 ? nullptr
                                           : a.slab + ((int64_t)tile.split * plan.rest + tile.rest) * (BM * CG * BN / 4) +
@@ -838,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         product_epilogue<CG>(a, base + C::OUT_OFF + (uint32_t)(warp - 4) * 4096, lane, i, n, on, tile.n, half, slab_row, x);
       }
     }
-    if constexpr (KIND == GRAD || KIND == GRAD2 || KIND == GRAD3) {
+    if constexpr (KIND == GRAD || KIND == GRAD3) {
       if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }

@@ -225,3 +225,31 @@ def test_fp32_wide_rows_in_a_replayed_graph(env):
         eager = check_all(env, a, b, target, weight)
         for k in out:
             assert torch.equal(out[k], eager[k]), k
+
+
+@pytest.mark.parametrize("N,part", [(4096, 100), (257, 256), (3000, 256), (300, 1)])
+def test_gradient_of_few_rows_among_many(env, N, part):
+    """bf16 gradients over few rows that take part carry one rounding, the
+    output's, whatever N is: the root mean square of the error is that of the
+    exact gradient rounded once.  (Another rounding of dz would make it 1.4 of
+    that; 16 bits of dz and fp32 sums add less than a hundredth.)"""
+    rlt, torch = env
+    V, d = 2000, 128
+    h, w, _, weight = make(torch, N, V, d, "bf16", seed=part)
+    g = torch.Generator().manual_seed(part)
+    target = torch.full((N,), -1, dtype=torch.int32)
+    rows = torch.randperm(N, generator=g)[:part]
+    target[rows] = torch.randint(0, V, (part,), generator=g, dtype=torch.int32)
+    target = target.cuda()
+    ids = torch.full((N, 3), -1, dtype=torch.int32)
+    ids[rows] = torch.randint(0, V, (part, 3), generator=g, dtype=torch.int32)
+    teacher = torch.randn(N, 3, generator=g).cuda()
+    for got, lists, T in ((ce(env, h, w, target, weight), {"target": target}, 1.0),
+                          (kl(env, h, w, ids.cuda(), teacher, 0.8, weight), {"ids": ids.cuda(), "teacher": teacher}, 0.8)):
+        ref = reference(torch, h, w, T=T, weight=weight, **lists)
+        for k in ("dh", "dw"):
+            within(torch, got[k], ref[k], k)
+            exact = ref[k][0]
+            once = (exact.to(torch.bfloat16).double() - exact).square().mean().sqrt()
+            off = (got[k].double() - exact).square().mean().sqrt()
+            assert off <= 1.05 * once, (k, (off / once).item())
