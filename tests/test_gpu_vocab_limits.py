@@ -227,6 +227,42 @@ def test_fp32_wide_rows_in_a_replayed_graph(env):
             assert torch.equal(out[k], eager[k]), k
 
 
+# ------------------------------------------------------------------ accuracy where the bounds of sums are wide
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,d", [(1100, 5000, 2048), (300, 9000, 1600), (100, 3001, 2112)])
+def test_logits_of_long_rows(env, N, V, d, dtype):
+    """Pairs of CTAs, several rounds of tiles and several tensor-memory sums.
+    The bound on a logit's error here is of root mean square, (2/3) d^1.5 u s
+    with s that of the products h w: every one of d additions off, all one
+    way, by u times a partial sum of sqrt(k) s.  It is below the 2^-12 sqrt(d)
+    s that an fp32 operand's lost lower half would leave.  The logit is logp +
+    lse, each of them a rounding of its own and the sum's 2^-21 of lse."""
+    rlt, torch = env
+    h, w, target, weight = make(torch, N, V, d, dtype, seed=d, ignored=0.3)
+    got = ce(env, h, w, target, weight)
+    ref = reference(torch, h, w, target=target, weight=weight)
+    for k in ("loss", "lse", "dh", "dw"):
+        within(torch, got[k], ref[k], k)
+    on = target >= 0
+    z = (h[on].double() * w[target[on].long()].double()).sum(1)
+    s = (h[on].double().square() * w[target[on].long()].double().square()).mean().sqrt()
+    off = (got["loss"][on].double() + got["lse"][on].double() - z).square().mean().sqrt()
+    stored = 2.0 ** -21 * got["lse"][on].double().abs().max()
+    assert off <= 2 / 3 * d ** 1.5 * U * s + stored, (off.item(), s.item())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 2, 8])
+def test_few_rows_past_the_streaming_kernel(env, N, dtype):
+    """d over 6,400: the rows of h no longer fit the streaming kernel."""
+    rlt, torch = env
+    h, w, target, weight = make(torch, N, 301, 6504, dtype, seed=N, ignored=0.0)
+    got = ce(env, h, w, target, weight)
+    ref = reference(torch, h, w, target=target, weight=weight)
+    for k in ("loss", "lse", "dh", "dw"):
+        within(torch, got[k], ref[k], k)
+
+
 @pytest.mark.parametrize("N,part", [(4096, 100), (257, 256), (3000, 256), (300, 1)])
 def test_gradient_of_few_rows_among_many(env, N, part):
     """bf16 gradients over few rows that take part carry one rounding, the
@@ -253,3 +289,35 @@ def test_gradient_of_few_rows_among_many(env, N, part):
             once = (exact.to(torch.bfloat16).double() - exact).square().mean().sqrt()
             off = (got[k].double() - exact).square().mean().sqrt()
             assert off <= 1.05 * once, (k, (off / once).item())
+
+
+# ------------------------------------------------------------------ long sorts
+@pytest.mark.parametrize("V", [200, 255, 256, 32000, 65535, 65536, 70000])
+@pytest.mark.parametrize("N,dist", [(16384, "uniform"), (16385, "zipf"), (20001, "uniform"), (65536, "zipf")])
+def test_embedding_gradient_of_many_ids(env, N, dist, V):
+    """One block's sort at its largest and several blocks', in one to three
+    passes (keys go to V, the ids that do not count), a tenth of the ids
+    outside, into a table of its own, a slice of rows off the 16-byte grid, and
+    one that is added to."""
+    rlt, torch = env
+    d = 24 if N < 60000 else 8
+    g = torch.Generator().manual_seed(N + V)
+    tok = torch.randint(0, V, (N,), generator=g) if dist == "uniform" else (V * torch.rand(N, generator=g) ** 6).long().clamp(max=V - 1)
+    out = torch.rand(N, generator=g) < 0.1
+    tok[out] = torch.tensor([-1, V, V + 1, 2 ** 31 - 1, -2 ** 31])[torch.randint(0, 5, (int(out.sum()),), generator=g)]
+    tok = tok.to(torch.int32).cuda()
+    dout = torch.randn(N, d, generator=g).cuda()
+    dout[out.cuda()] = math.nan
+    value, bound = embed_reference(torch, dout, tok, V, 1.5, torch.float32)
+    table = torch.full((V, d), 7.0, device="cuda")
+    rlt.rlt_op_embed_backward(dout, tok, table, scale=1.5)
+    within(torch, table, (value, bound), "whole")
+    absent = torch.bincount(tok[~out.cuda()].long(), minlength=V) == 0
+    assert (table[absent] == 0).all()
+    wide = torch.full((V, d + 5), 9.0, device="cuda")
+    rlt.rlt_op_embed_backward(dout, tok, wide[:, 3:3 + d], scale=1.5)
+    assert torch.equal(wide[:, 3:3 + d], table)
+    assert (wide[:, :3] == 9).all() and (wide[:, 3 + d:] == 9).all()
+    half = torch.full((V, d), 2.0, dtype=torch.bfloat16, device="cuda")
+    rlt.rlt_op_embed_backward(dout, tok, half, scale=1.5, accumulate=True)
+    within(torch, half, (value + 2, bound + half_step(half.dtype) * (value + 2).abs() + U * (value + 2).abs()), "added")
