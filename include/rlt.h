@@ -477,7 +477,11 @@ typedef struct rlt_vocab {
  * belongs to the call until its work on `stream` is done: calls that may
  * overlap on the GPU, replays of captured graphs among them, need their own.
  * The calls allocate nothing, wait for nothing on the host, and can be
- * captured into a graph.  Results do not depend on timing.
+ * captured into a graph.  Results do not depend on timing; a row's last bits
+ * may depend on how many rows share the call (few rows are streamed, many go
+ * to the tensor cores in larger tiles), so calls that have to agree bit by bit
+ * have to agree in N too.  A forward call holds 8 bytes per row and 32 to 128
+ * columns of the vocabulary besides copies of operands.
  * No output may share memory with an operand, the workspace or another output
  * (RLT_E_INVAL); slices of one buffer that lie between each other's rows do
  * not. */

@@ -4,14 +4,15 @@
 // z[n][v] = inv_t * sum_k h[n][k] w[v][k].  Forward: every tile of the logits
 // leaves (maximum, sum of exponentials) per row and up to 128 columns, joined
 // in a fixed order into lse[n].  Backward, one piece of the vocabulary at a time:
-// g[n][v] = c[n] (exp(z - lse[n]) - q[n][v]) as bf16 into a buffer of the
-// piece's width, then dh += g w and dw = g^T h.  The piece bounds the buffer;
-// the logits are recomputed, never kept.
+// g[n][v] = c[n] (exp(z - lse[n]) - q[n][v]) as one to three bf16 planes into a
+// buffer of the piece's width, then dh += g w and dw = g^T h.  The piece bounds
+// the buffer; the logits are recomputed, never kept.
 //
 // Rows that take no part (no target, an empty list, weight 0 in the backward)
 // are left out before the contractions: the rows that remain are gathered, in
-// order, into one bf16 operand, and every extent follows their count on the
-// device.
+// order, into an operand of 16-bit planes (bf16 rows as they are; fp32 rows as
+// two of fp16, three of bf16, or both), and every extent follows their count on
+// the device.
 #include <cuda_fp16.h>
 #include <math.h>
 

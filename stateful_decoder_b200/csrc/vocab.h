@@ -46,7 +46,8 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
 cudaError_t embed_lookup(const void* emb, int64_t ld_emb, int emb_dtype, int V, int d, const int32_t* tok, int N,
                          float scale, void* out, int64_t ld_out, int out_dtype, cudaStream_t st);
 
-// demb[v] (+)= scale * sum of dout[n] over tok[n] = v, in order of n.
+// demb[v] (+)= scale * sum of dout[n] over tok[n] = v, in order of n within the
+// runs that the sorted rows are cut into, then in order of the runs.
 size_t embed_backward_workspace_bytes(int N, int V, int d);
 cudaError_t embed_backward(const void* dout, int64_t ld_dout, int dout_dtype, const int32_t* tok, int N, int V, int d,
                            float scale, void* demb, int64_t ld_demb, int demb_dtype, int accumulate, void* ws,

@@ -119,7 +119,7 @@ struct Args {
   int a_rows;             // rows of A that a tile loads (fewer than BM when M is: the rest are never looked at)
   int units;              // CTAs or pairs on the device
   int max_splits;         // K ranges of the last round's tiles at most (DH, DW); see split_rule
-  int a_row, a_k, b_row, b_k;  // coordinate offsets of the operands
+  int b_row, b_k;         // coordinate offsets of B: a piece of the vocabulary
   // STATS, GRAD
   int early;              // operands are older than the kernel before this one: loads do not wait for it
   RowList list;
@@ -700,10 +700,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     const uint32_t bytes = (uint32_t)(a.a_rows * CG + a.bn) * (BK * 2);
-    const int k_off = is_a ? a.a_k : a.b_k;
+    const int k_off = is_a ? 0 : a.b_k;
     for (int t = first; t < plan.tiles && ok; t += step) {
       const Tile tile = plan.at(t);
-      const int row = is_a ? tile.m * BM * CG + rank * BM + a.a_row : tile.n * a.bn + rank * (a.bn / CG) + a.b_row;
+      const int row = is_a ? tile.m * BM * CG + rank * BM : tile.n * a.bn + rank * (a.bn / CG) + a.b_row;
       int turn = tile.kb0 / max(1, plan.kb), kt = tile.kb0 - turn * plan.kb;
       for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
         if (!mbar_wait(empty + 8 * slot, phase ^ 1u)) {
