@@ -502,8 +502,9 @@ int32_t rlt_op_cross_entropy(const rlt_vocab* a, const int32_t* target_dev, floa
  * dw_dev [V][d] is written whole or, with accumulate_dw, added to.  Either
  * may be NULL, not both.  Sums are fp32; with bf16 operands dz is rounded to
  * bf16 once, as an operand of the two products (to 16 bits where at most 256
- * rows take part).  The workspace holds up to 512 MB of dz, or 2048 columns of
- * it where that is more.
+ * rows take part), and dh gets back in fp32 what that took from its row's
+ * listed entries (the target's; a teacher's).  The workspace holds up to 512 MB
+ * of dz, or 2048 columns of it where that is more.
  * Errors: as rlt_op_cross_entropy. */
 int32_t rlt_op_cross_entropy_backward(const rlt_vocab* a, const int32_t* target_dev, const float* lse_dev,
                                       const float* weight_dev, void* dh_dev, int64_t ld_dh, void* dw_dev,

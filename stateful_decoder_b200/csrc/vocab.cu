@@ -579,6 +579,99 @@ __global__ void __launch_bounds__(256) slab_sum_kernel(const SlabSum a) {
   }
 }
 
+// ------------------------------------------------------------------ residuals
+// acc[i] (+)= sum_k resid[n][k] w[ids[n][k]]: what rounding g to bf16 took from
+// dh at the row's listed ids.  Those are the entries that carry dh (the target
+// has p - 1 where others have their p), and a sum near zero, of rows of w that
+// point the same way, shows their rounding most: dh of bf16 operands was off by
+// 1.35 to 1.57 of its own rounding with one plane of g, and is by 1.00 to 1.14
+// with its listed entries whole (234 cases of d = 17 to 400); a second plane
+// would cost a quarter of the backward.  One warp per row; entries whose
+// residual is below 1 / (8 sqrt(K)) of the row's largest, together an eighth of
+// it, are left out, so a list costs few rows of w.  Where fine_rows or fewer
+// take part g has both planes and nothing is missing.
+__global__ void __launch_bounds__(256) residual_kernel(RowList list, const float* resid, const int32_t* row_of,
+                                                       const int32_t* count, int fine_rows, int V, const bf16* w,
+                                                       int64_t ld_w, int d, float* acc, int add) {
+  griddep_enter();
+  __shared__ int32_t ids_s[8][256];
+  __shared__ float r_s[8][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * 8 + warp;
+  const int rows = *count;
+  if (i >= rows) return;
+  int32_t* ids = ids_s[warp];
+  float* rs = r_s[warp];
+  int kept = 0;
+  if (rows > fine_rows) {
+    const int64_t e0 = (int64_t)row_of[i] * list.K;
+    int32_t id[8];
+    float r[8], m = 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int k = u * 32 + lane;
+      id[u] = k < list.K ? list.ids[e0 + k] : -1;
+      r[u] = id[u] >= 0 && id[u] < V ? resid[e0 + k] : 0.f;
+      m = fmaxf(m, fabsf(r[u]));
+    }
+    m = warp_max(m);
+    const float least = list.K == 1 ? 0.f : m * 0.125f * rsqrtf((float)list.K);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool keep = !(fabsf(r[u]) <= least);  // NaN is kept
+      const unsigned in = __ballot_sync(0xffffffffu, keep);
+      if (keep) {
+        const int at = kept + __popc(in & ((1u << lane) - 1));
+        ids[at] = id[u];
+        rs[at] = r[u];
+      }
+      kept += __popc(in);
+    }
+    __syncwarp();
+  }
+  float* out = acc + i * d;
+  const bool vec = d % 4 == 0;
+  for (int c0 = lane * 8; c0 < d; c0 += 1024) {
+    float s[4][8] = {};
+    for (int e = 0; e < kept; ++e) {
+      const bf16* row = w + (int64_t)ids[e] * ld_w;
+      const float r = rs[e];
+      float x[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = c0 + u * 256;
+        if (c + 8 <= d) {
+          load8(row + c, x[u]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[u][j] = c + j < d ? to_f32(row[c + j]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[u][j] = fmaf(r, x[u][j], s[u][j]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + u * 256;
+      if (vec && c + 8 <= d) {
+        if (add) {
+          float old[8];
+          load8(out + c, old);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[u][j] += old[j];
+        }
+        store8(out + c, s[u]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < d) out[c + j] = add ? s[u][j] + out[c + j] : s[u][j];
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ few rows
 // Statistics of up to 8 rows: bound by reading w once, so w goes through
 // registers (16-byte loads, the next step's in flight under this one's
@@ -895,7 +988,7 @@ cudaError_t contract(const Operands& o, const Args& a, cudaStream_t st) {
 struct Layout {
   size_t sid = 0, sq = 0, slogq = 0, some = 0, row_of = 0, count = 0, h = 0, w = 0, h16 = 0, w16 = 0, h_inv = 0,
          w_inv = 0, h_least = 0, w_least = 0, part = 0, zsel = 0, g = 0,
-         dh = 0, dw = 0, acc = 0, total = 0;
+         dh = 0, dw = 0, acc = 0, resid = 0, total = 0;
   int planes = 1, terms = 1;      // bf16 planes of h and w; products of h w^T
   int g_planes = 1, g_terms = 1;  // of g, and of its products
   bool few = false, gather = true, pack_w = false;
@@ -903,6 +996,7 @@ struct Layout {
   int64_t ld = 0;    // row distance of gathered and packed operands
   int bn = BN, parts = 0, piece = 0, pieces = 0;
   int dh_splits = 1, dw_splits = 1;  // at most
+  bool residuals = false;  // g may be one plane: dh gets back what rounding took from its listed entries
 };
 
 bool tma_ready(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
@@ -1040,7 +1134,9 @@ Layout layout(const VocabLoss& p, int backward) {
   // rows).  Over few rows single entries of g carry the gradients and their
   // rounding does not average: where up to kFineRows take part, a count that
   // only the device knows, a second plane takes it away, at 13 to 22 % of the
-  // backward's time (64 to 256 rows, V = 32000, d = 2048).
+  // backward's time (64 to 256 rows, V = 32000, d = 2048).  Over more rows dh,
+  // whose rows stay single, gets back what rounding took from their listed
+  // entries (residual_kernel).
   L.g_planes = f32 ? 3 : p.N <= kFineRows ? 2 : 1;  // at most, and what the cut of the work reckons with
   L.g_terms = f32 ? 6 : L.g_planes;
   // The piece: at most as wide as 512 MB of g allow (256 MB was 5 % slower at
@@ -1064,7 +1160,9 @@ Layout layout(const VocabLoss& p, int backward) {
   L.g = take((size_t)(f32 ? 3 * L.rows : std::max<int64_t>(L.rows, 2 * kFineRows)) * L.piece * 2);
   L.dw = take((size_t)slab_floats(L.piece, p.d, L.rows / BK * L.g_terms, &L.dw_splits) * 4);
   L.dh = take((size_t)slab_floats(p.N, p.d, (int64_t)L.piece / BK * L.g_terms, &L.dh_splits) * 4);
-  if (L.pieces > 1) L.acc = take((size_t)L.rows * p.d * 4);  // dh over the pieces
+  L.residuals = !f32 && p.N > kFineRows;
+  if (L.residuals) L.resid = take(n * p.K * 4);
+  if (L.pieces > 1 || L.residuals) L.acc = take((size_t)L.rows * p.d * 4);  // dh over the pieces, residuals
   return L;
 }
 
@@ -1319,6 +1417,8 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.bn = L.bn;
     a.chunk = logit_chunk(p.dtype, p.N, width, L.bn);
     a.fine_rows = fine ? kFineRows : 0;
+    const bool last = i + 1 == L.pieces, residuals = dh && L.residuals;
+    a.resid = residuals ? at<float>(ws, L.resid) : nullptr;
     Operands z = logit_operands(r, &G);
     if (fine) z.A2 = fine;
     VOCAB_TRY(p.dtype ? contract<GRAD>(z, a, st) : contract<GRAD3>(z, a, st));
@@ -1334,9 +1434,13 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
       c.K = width;
       c.b_k = v0;
       c.max_splits = L.dh_splits;
-      c.acc = L.pieces > 1 ? at<float>(ws, L.acc) : nullptr;
-      c.acc_in = i > 0;
-      c.acc_out = i + 1 < L.pieces;
+      c.acc = L.pieces > 1 || residuals ? at<float>(ws, L.acc) : nullptr;
+      c.acc_in = i > 0 || (residuals && last);
+      c.acc_out = !last;
+      if (residuals && last)
+        VOCAB_TRY(launch_pdl(residual_kernel, dim3((unsigned)((p.N + 7) / 8)), dim3(256), 0, st, r.list,
+                             (const float*)a.resid, r.row_of, r.count, kFineRows, p.V, r.w.p, r.w.ld, p.d, c.acc,
+                             (int)(i > 0)));
       VOCAB_TRY(product<DH>(p, Operands{G, r.w, nullptr, fine}, c, dh_slab, dh, ld_dh, 0, st));
     }
     if (dw) {

@@ -131,9 +131,10 @@ struct Args {
   float* zsel;            // [rows][K]
   const float* lse;
   const float* weight;
+  float* resid;           // [rows][K], GRAD of one plane: what rounding took from g at the row's listed ids, or null
   // DH, DW
   float4* slab;           // [splits][last round's tiles][BN / 4][rows of a tile]: a warp's rows side by side
-  float* acc;             // fp32 [rows][N]: the sum over pieces of K, or null
+  float* acc;             // fp32 [rows][N]: the sum over pieces of K and what rounding took, or null
   int acc_in, acc_out;    // add what acc holds; leave the sum there
   void* out;
   int64_t ld_out;
@@ -473,8 +474,15 @@ __device__ __forceinline__ void grad_epilogue(const Args& a, const CUtensorMap* 
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = cw * ex2(fmaf(v[j], a.scale, -l) * kLog2e);
       while (next >= v0 + c * 32 && next < v0 + min(c * 32 + 32, cols)) {
-        sub_at(v, next - v0 - c * 32, cw * (a.list.q ? a.list.q[n * a.list.K + pos] : 1.f));
+        const int id = next, slot = pos;
+        sub_at(v, id - v0 - c * 32, cw * (a.list.q ? a.list.q[n * a.list.K + pos] : 1.f));
         next = ++pos < a.list.K ? a.list.ids[n * a.list.K + pos] : kNoId;
+        if constexpr (PLANES == 1) {
+          if (a.resid) {  // of an id in several slots the last has it
+            const float g = pick(v, id - v0 - c * 32);
+            a.resid[n * a.list.K + slot] = next == id ? 0.f : g - to_f32(from_f32<bf16>(g));
+          }
+        }
       }
       if (c * 32 + 32 > cols) {
 #pragma unroll
@@ -583,10 +591,20 @@ __device__ __forceinline__ void product_epilogue(const Args& a, uint32_t stage, 
         }
         continue;
       }
-      if (on) {
+      if (on && a.acc_in) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < left) v[j] += a.acc[at + j];
+        for (int j = 0; j < 32; j += 8) {
+          if (j + 8 <= left && (a.N & 3) == 0) {
+            float old[8];
+            load8(a.acc + at + j, old);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j + e] += old[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (j + e < left) v[j + e] += a.acc[at + j + e];
+          }
+        }
       }
     }
     const int64_t at = n * a.ld_out + col0 + c * 32;
