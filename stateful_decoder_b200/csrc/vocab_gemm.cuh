@@ -40,9 +40,9 @@
 // chunk's MMAs.
 //
 // Bound by the tensor cores where there are rows enough: at 8,192 rows, V =
-// 32000, d = 2048, the tensor pipe is active 94 to 95 % of the time in all four
-// kinds and the power limit sets the clock (1.35 to 1.42 GHz): 655 us for
-// STATS, 1.64 PFLOP/s, and 1.54 to 1.59 in the others.  Two CTAs per tile
+// 32000, d = 2048, the tensor pipe is active 95 % of the time in all four
+// kinds and the power limit sets the clock (1.35 to 1.42 GHz): 651 us for
+// STATS, 1.65 PFLOP/s, and 1.56 to 1.58 in the others.  Two CTAs per tile
 // (256 x 256, each loads half of the columns' operand) took 8 % off a forward
 // and backward of 16,368 rows against one (128 x 256).
 #pragma once
