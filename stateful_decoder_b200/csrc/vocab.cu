@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(256, 4) gather_kernel(const Gather g) {
   uint32_t least = 0xffffffffu;
   const int b = (int)blockIdx.x;
   gather_block<T>(g, b, red, &least);
-  if (sizeof(T) == 4 && (b < g.row_blocks || b >= g.row_blocks + g.pad_blocks)) {
+  if (sizeof(T) == 4 && g.h_least && (b < g.row_blocks || b >= g.row_blocks + g.pad_blocks)) {
     least = __reduce_min_sync(0xffffffffu, least);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = (int)least;
     __syncthreads();
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(256) residual_kernel(RowList list, const float
 }
 
 // ------------------------------------------------------------------ few rows
-// Statistics of up to 8 rows: bound by reading w once, so w goes through
+// Statistics, or g, of up to 8 rows: bound by reading w once, so w goes through
 // registers (16-byte loads, the next step's in flight under this one's
 // products) and h through shared memory, in fp32.  A warp takes two to four
 // rows of w at a time against all NB rows of h; the sums of its lanes are added by
@@ -714,10 +714,26 @@ struct Raw<float> {
   }
 };
 
-template <typename T, int NB>
+//
+// fp32 rows whose statistics came from here get their g from here too (FewGrad),
+// from the same sums: the tensor cores' logits lie a few 1e-7 of themselves
+// towards zero, which an lse of the same logits takes out of p = exp(z - lse)
+// and an exact one does not (gradients of 1 to 8 rows were off by up to 5.7e-6
+// where fp32 matrix products leave 1e-6; now by 1.3e-6 at most in 400 cases).
+// The backward of 8 rows, V = 32000, d = 2048 takes 457 us for 491 with the
+// logits from fp16 planes, that of 8, V = 4000, d = 512 48 for 56.
+struct FewGrad {
+  bf16* g;  // three planes of [rows][ld], from row 0 of w on; rows up to 64 and columns up to 64 are filled with zeros
+  int64_t plane, ld;
+  const int32_t *row_of, *count;
+  const float *lse, *weight;
+  int v0;   // first row of w in the vocabulary
+};
+template <typename T, int NB, bool GRADIENT>
 __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld_h, const T* w, int64_t ld_w, int N,
                                                           int V, int d, int vec, float scale, RowList list, int early,
-                                                          float2* part, int64_t part_ld, float* zsel) {
+                                                          float2* part, int64_t part_ld, float* zsel,
+                                                          const FewGrad fg) {
   constexpr int R = kFewW<NB>;
   constexpr int U = (sizeof(T) == 2 ? 8 : 4) / R;  // groups of 256 columns per step
   extern __shared__ float4 hs[];  // [NB][2][d8]: the two halves of every group of eight
@@ -759,7 +775,33 @@ __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld
   if (early) griddep_enter();
   __syncthreads();
   const int n = lane % NB, r = lane / NB;  // what this lane finishes
-  const bool mine = lane < R * NB && n < N;
+  bool mine = lane < R * NB && n < N;
+  [[maybe_unused]] float cw = 0.f, l = 0.f;
+  [[maybe_unused]] bf16* g_row = nullptr;  // of row n, if it takes part
+  if constexpr (GRADIENT) {
+    const int count = *fg.count;
+    int at = -1;
+    for (int i = 0; i < count; ++i)
+      if (fg.row_of[i] == n) at = i;
+    mine = mine && at >= 0;
+    if (mine) {
+      cw = fg.weight[n] * scale;
+      l = fg.lse[n];
+      g_row = fg.g + at * fg.ld;
+    }
+    // what the products read besides: rows behind the last, columns behind V
+    const int64_t thread = (int64_t)blockIdx.x * 512 + threadIdx.x, threads = (int64_t)gridDim.x * 512;
+    const int chunks = (V + BK - 1) / BK * (BK / 8), rows = count > 0 ? BK - count : 0;
+    for (int64_t e = thread; e < (int64_t)3 * rows * chunks; e += threads) {
+      const int64_t row = e / chunks, c = e - row * chunks;
+      *reinterpret_cast<uint4*>(fg.g + row / rows * fg.plane + (count + row % rows) * fg.ld + c * 8) = make_uint4(0, 0, 0, 0);
+    }
+    const int tail = chunks * 8 - V;
+    for (int64_t e = thread; e < (int64_t)3 * count * tail; e += threads) {
+      const int64_t row = e / tail;
+      fg.g[row / count * fg.plane + row % count * fg.ld + V + e % tail] = from_f32<bf16>(0.f);
+    }
+  }
   int pos = 0, next = mine ? list.ids[(int64_t)n * list.K] : kNoId;
   float m = -INFINITY, s = 0.f;
   float acc[R * NB];
@@ -845,20 +887,36 @@ __global__ void __launch_bounds__(512, 1) few_rows_kernel(const T* h, int64_t ld
     const int64_t v = v0 + r;
     if (mine && v < V) {
       const float z = acc[0] * scale;
-      while (next < v && pos + 1 < list.K) next = list.ids[(int64_t)n * list.K + ++pos];
-      while (next == v) {
-        zsel[(int64_t)n * list.K + pos] = z;
-        next = ++pos < list.K ? list.ids[(int64_t)n * list.K + pos] : kNoId;
+      const int64_t id = GRADIENT ? v + fg.v0 : v;
+      while (next < id && pos + 1 < list.K) next = list.ids[(int64_t)n * list.K + ++pos];
+      if constexpr (GRADIENT) {
+        float g = cw * expf(z - l);
+        while (next == id) {
+          g -= cw * (list.q ? list.q[(int64_t)n * list.K + pos] : 1.f);
+          next = ++pos < list.K ? list.ids[(int64_t)n * list.K + pos] : kNoId;
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const bf16 b = from_f32<bf16>(g);
+          g_row[p * fg.plane + v] = b;
+          g -= to_f32(b);
+        }
+      } else {
+        while (next == id) {
+          zsel[(int64_t)n * list.K + pos] = z;
+          next = ++pos < list.K ? list.ids[(int64_t)n * list.K + pos] : kNoId;
+        }
+        const float mn = fmaxf(m, z), ref = mn > -INFINITY ? mn : 0.f;
+        s = (s == 0.f ? 0.f : s * expf(m - ref)) + expf(z - ref);
+        m = mn;
       }
-      const float mn = fmaxf(m, z), ref = mn > -INFINITY ? mn : 0.f;
-      s = (s == 0.f ? 0.f : s * expf(m - ref)) + expf(z - ref);
-      m = mn;
     }
     __syncwarp();
     v0 += (int64_t)stride * R;
 #pragma unroll
     for (int i = 0; i < R * NB; ++i) acc[i] = 0.f;
   }
+  if constexpr (GRADIENT) return;
   sums[warp][lane] = make_float2(m, s);
   __syncthreads();
   if (warp == 0 && lane < NB && lane < N) {  // the block's statistics of row `lane`
@@ -1098,14 +1156,15 @@ Layout layout(const VocabLoss& p, int backward) {
     L.slogq = take(n * p.K * 4);
     L.some = take(n * 4);
   }
-  L.few = !backward && p.N <= few_rows_limit(p.dtype) && (size_t)kFewRows * round_up(p.d, 8) * 4 <= kFewSmem;
+  const bool few = p.N <= few_rows_limit(p.dtype) && (size_t)kFewRows * round_up(p.d, 8) * 4 <= kFewSmem;
+  L.few = few && (!backward || f32);  // (of bf16 rows g is rounded far coarser than where its logits differ)
   // A forward pass over one row tile has nothing to gain from leaving rows
   // out, and its rows do not mix: it reads h where it is.
-  L.gather = !L.few && (f32 || backward || p.N > BM || !tma_ready(p.h, p.ld_h));
+  L.gather = backward || (!L.few && (f32 || p.N > BM || !tma_ready(p.h, p.ld_h)));
   // w is read where it is whenever TMA can: rows that do not start on 128-byte
   // lines cost up to 27 % of a contraction's rate (d = 1000), but a copy on
   // every call costs more (2048 rows, V = 32000: 107 us with it, 94 without).
-  L.pack_w = !L.few && (f32 || !tma_ready(p.w, p.ld_w));
+  L.pack_w = (backward || !L.few) && (f32 || !tma_ready(p.w, p.ld_w));
   if (L.gather) {
     L.row_of = take(n * 4);
     L.count = take(4);
@@ -1240,7 +1299,7 @@ cudaError_t prepare(const VocabLoss& p, const Layout& L, void* ws, const float* 
     g.w_plane = (int64_t)p.V * L.ld;
     r->zw = r->w = Matrix{g.w_out, p.V, p.d, L.ld, g.w_plane, L.planes};
   }
-  if (p.dtype == 0) {
+  if (p.dtype == 0 && !L.few) {
     g.h16 = at<__half>(ws, L.h16);
     g.w16 = at<__half>(ws, L.w16);
     r->h_inv = g.h_inv = at<float>(ws, L.h_inv);
@@ -1307,24 +1366,34 @@ Args args_of(const VocabLoss& p, const Layout& L, const Prepared& r) {
   return a;
 }
 
+// Statistics into part and zsel, or (fg) g of the `rows` rows of w from fg->v0 on.
 template <typename T, int NB>
-cudaError_t few_rows(const VocabLoss& p, const Layout& L, const RowList& list, float2* part, float* zsel,
-                     cudaStream_t st) {
+cudaError_t few_rows(const VocabLoss& p, const RowList& list, float2* part, float* zsel,
+                     const FewGrad* fg, int rows, cudaStream_t st) {
   const size_t smem = (size_t)NB * round_up(p.d, 8) * 4;
-  VOCAB_TRY((set_smem<few_rows_kernel<T, NB>>((int)kFewSmem)));
   const int vec = vector_rows(p.w, p.ld_w, p.dtype);
-  return launch_pdl(few_rows_kernel<T, NB>, dim3((unsigned)L.parts), dim3(512), smem, st, static_cast<const T*>(p.h),
-                    p.ld_h, static_cast<const T*>(p.w), p.ld_w, p.N, p.V, p.d, vec, p.inv_t, list,
-                    (int)(p.teacher != nullptr), part,
-                    (int64_t)kFewRows, zsel);
+  const dim3 grid((unsigned)std::min<int64_t>(kSmCount, ((int64_t)rows + 15) / 16));
+  const T *h = static_cast<const T*>(p.h), *w = static_cast<const T*>(p.w);
+  if constexpr (sizeof(T) == 4) {
+    if (fg) {
+      VOCAB_TRY((set_smem<few_rows_kernel<T, NB, true>>((int)kFewSmem)));
+      return launch_pdl(few_rows_kernel<T, NB, true>, grid, dim3(512), smem, st, h, p.ld_h, w + fg->v0 * p.ld_w, p.ld_w,
+                        p.N, rows, p.d, vec, p.inv_t, list, 0, part, (int64_t)kFewRows, zsel, *fg);
+    }
+  }
+  VOCAB_TRY((set_smem<few_rows_kernel<T, NB, false>>((int)kFewSmem)));
+  return launch_pdl(few_rows_kernel<T, NB, false>, grid, dim3(512), smem, st, h, p.ld_h, w, p.ld_w, p.N, rows, p.d, vec,
+                    p.inv_t, list, (int)(p.teacher != nullptr), part, (int64_t)kFewRows, zsel, FewGrad{});
 }
-cudaError_t few_rows_of(const VocabLoss& p, const Layout& L, const RowList& list, float2* part, float* zsel,
-                        cudaStream_t st) {
-  if (p.dtype) return p.N == 1 ? few_rows<bf16, 1>(p, L, list, part, zsel, st) : few_rows<bf16, 2>(p, L, list, part, zsel, st);
-  if (p.N == 1) return few_rows<float, 1>(p, L, list, part, zsel, st);
-  if (p.N == 2) return few_rows<float, 2>(p, L, list, part, zsel, st);
-  if (p.N <= 4) return few_rows<float, 4>(p, L, list, part, zsel, st);
-  return few_rows<float, 8>(p, L, list, part, zsel, st);
+cudaError_t few_rows_of(const VocabLoss& p, const RowList& list, float2* part, float* zsel,
+                        const FewGrad* fg, int rows, cudaStream_t st) {
+  if (p.dtype)
+    return p.N == 1 ? few_rows<bf16, 1>(p, list, part, zsel, fg, rows, st)
+                    : few_rows<bf16, 2>(p, list, part, zsel, fg, rows, st);
+  if (p.N == 1) return few_rows<float, 1>(p, list, part, zsel, fg, rows, st);
+  if (p.N == 2) return few_rows<float, 2>(p, list, part, zsel, fg, rows, st);
+  if (p.N <= 4) return few_rows<float, 4>(p, list, part, zsel, fg, rows, st);
+  return few_rows<float, 8>(p, list, part, zsel, fg, rows, st);
 }
 
 // A product of g into typed rows, K split where the rule says so.
@@ -1340,8 +1409,6 @@ cudaError_t product(const VocabLoss& p, const Operands& o, Args a, float4* slab,
   a.out_bf16 = p.dtype;
   a.accumulate = accumulate;
   a.vec = vector_rows(out, ld, p.dtype);
-  // bf16 gradients: a sum's drift over 4096 of k (8e-6) is far below their own rounding
-  a.chunk = p.dtype ? 64 : 4;
   VOCAB_TRY(contract<KIND>(o, a, st));
   if (a.max_splits == 1) return cudaSuccess;
   const SlabSum s{slab,  a.M,    a.N,          a.K, a.m_count, a.k_count,  a.terms,  a.terms2, a.fine_rows,
@@ -1366,7 +1433,7 @@ cudaError_t vocab_forward(const VocabLoss& p, float* loss, float* lse, void* ws,
   float2* part = at<float2>(ws, L.part);
   float* zsel = at<float>(ws, L.zsel);
   if (L.few) {
-    VOCAB_TRY(few_rows_of(p, L, r.list, part, zsel, st));
+    VOCAB_TRY(few_rows_of(p, r.list, part, zsel, nullptr, p.V, st));
   } else {
     Args a = args_of(p, L, r);
     a.M = p.N;
@@ -1421,11 +1488,21 @@ cudaError_t vocab_backward(const VocabLoss& p, const float* lse, const float* we
     a.resid = residuals ? at<float>(ws, L.resid) : nullptr;
     Operands z = logit_operands(r, &G);
     if (fine) z.A2 = fine;
-    VOCAB_TRY(p.dtype ? contract<GRAD>(z, a, st) : contract<GRAD3>(z, a, st));
+    if (L.few) {
+      const FewGrad fg{const_cast<bf16*>(G.p), G.plane, G.ld, r.row_of, r.count, lse, weight, v0};
+      VOCAB_TRY(few_rows_of(p, r.list, nullptr, nullptr, &fg, width, st));
+    } else {
+      VOCAB_TRY(p.dtype ? contract<GRAD>(z, a, st) : contract<GRAD3>(z, a, st));
+    }
     Args b = args_of(p, L, r);
     b.terms = fine ? 1 : 6;
     b.terms2 = 2;
     b.fine_rows = a.fine_rows;
+    // k-blocks per tensor-memory sum.  bf16 gradients: a sum's drift over 4096
+    // of k (8e-6) is far below their own rounding.  Few fp32 rows: a single
+    // entry of g is most of a sum, and what comes after it drifts by 8 of its
+    // last places over 256 of k; there the extra sums hide behind w.
+    b.chunk = p.dtype ? 64 : L.few ? 1 : 4;
     if (dh) {
       Args c = b;
       c.M = p.N;

@@ -329,6 +329,63 @@ def test_dh_keeps_its_listed_entries_whole(env, N, V, d, K, lean):
     assert err.sqrt() <= 1.1 * (once + rest).sqrt(), ((err / (once + rest)).sqrt().item(), (err / once).sqrt().item())
 
 
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5, 8, 9, 64])
+def test_fp32_probabilities_of_the_backward_sum_to_one(env, N):
+    """The backward's logits have the errors of those the lse was made of, so
+    sum_v p - 1 is lse's own rounding, half a step of it, and the roundings of
+    the exponentials, planes and sums (4 + 1 + 24 u for the terms up to 1, and
+    4 additions towards zero of 2 u in tensor memory: 40 u).  A w whose first
+    column is 1 (and none of h) shows it as dh's first: weight (sum p - 1).
+    Logits of about 80: half a step of lse is 64 u."""
+    rlt, torch = env
+    V, d = 1500, 1001
+    for seed in range(4):
+        h, w, target, _ = make(torch, N, V, d, "f32", seed=seed, ignored=0.0)
+        h, weight = 25 * h, torch.ones(N, device="cuda")
+        h[:, 0], w[:, 0] = 0.0, 1.0
+        got = ce(env, h, w, target, weight)
+        half = torch.exp2(torch.floor(torch.log2(got["lse"].double()))) * U
+        off = got["dh"][:, 0].double().abs()
+        assert (off <= half + 40 * U).all(), (off / U, half / U)
+        ids, teacher = make_list(torch, N, V, 30, seed=seed, empty=0.0)
+        got = kl(env, h, w, ids, teacher, 1.0, weight)  # sum q is 1 to 2 u a term
+        assert (got["dh"][:, 0].double().abs() <= half + (40 + 60) * U).all()
+
+
+@pytest.mark.parametrize("N", [1, 3, 8])
+def test_few_fp32_rows_some_left_out(env, N):
+    """Odd widths, rows apart and off the grid, rows left out among the few, a
+    vocabulary in pieces, gradients added to and one at a time."""
+    rlt, torch = env
+    for V, d in ((17, 5), (333, 75), (1000, 264), (400_003, 4)):
+        h0, w0, target, weight = make(torch, N, V, d, "f32", seed=V, ignored=0.0)
+        hb, wb = (torch.full((x.shape[0], d + 3), math.nan, device="cuda") for x in (h0, w0))
+        h, w = hb[:, 1:1 + d], wb[:, 2:2 + d]
+        h.copy_(h0)
+        w.copy_(w0)
+        if N > 2:
+            target[0], weight[2] = -1, 0.0
+            h[0], h[2] = math.nan, math.inf
+            h0[0] = h0[2] = 0.0
+        want = reference(torch, h0, w0, target=target, weight=weight)
+        lse, loss = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+        rlt.rlt_op_cross_entropy(h0, w0, target, loss, lse)
+        dh, dw = torch.full((N, d), 7.0, device="cuda"), torch.full((V, d), 7.0, device="cuda")
+        rlt.rlt_op_cross_entropy_backward(h, w, target, lse, weight, dh=dh, dw=dw)
+        within(torch, dh, want["dh"], "dh")
+        within(torch, dw, want["dw"], "dw")
+        again = torch.full((V, d), 2.0, device="cuda")
+        rlt.rlt_op_cross_entropy_backward(h, w, target, lse, weight, dw=again, accumulate=True)
+        value, bound = want["dw"]
+        within(torch, again, (value + 2, bound + U * (value + 2).abs()), "dw added")
+        one = torch.empty_like(dh)
+        rlt.rlt_op_cross_entropy_backward(h, w, target, lse, weight, dh=one)
+        assert torch.equal(one, dh)
+        none = torch.full((V, d), 7.0, device="cuda")
+        rlt.rlt_op_cross_entropy_backward(h, w, torch.full_like(target, -1), lse, weight, dh=dh, dw=none)
+        assert (dh == 0).all() and (none == 0).all()
+
+
 # ------------------------------------------------------------------ long sorts
 @pytest.mark.parametrize("V", [200, 255, 256, 32000, 65535, 65536, 70000])
 @pytest.mark.parametrize("N,dist", [(16384, "uniform"), (16385, "zipf"), (20001, "uniform"), (65536, "zipf")])
